@@ -34,6 +34,11 @@
  *                                     returns the pair (output, lse)).
  *   attn_prefill_paged                chunked prefill whose keys and values sit
  *                                     in the paged cache.
+ *   attn_prefill_packed               the prefill of sequences of different
+ *                                     lengths, packed one after another.
+ *   attn_prefill_packed_paged         the same with keys and values in the paged
+ *                                     cache: a chunk of its own length of each
+ *                                     sequence.
  *   attn_prefill_host                 the prefill from and to host memory, its
  *                                     copies overlapped with the kernels.
  *   attn_decode_step_host             one decode step from and to host memory:
@@ -44,6 +49,8 @@
  *   attn_decode_paged_noalloc         the decode with a fixed scratch array
  *                                     instead of a workspace.
  *   attn_kv_append, attn_kv_append_fp8  write new tokens' K/V into the cache.
+ *   attn_kv_append_rope, attn_kv_append_rope_fp8  the same for packed tokens, with
+ *                                     q and k rotated by position on the way.
  *   attn_page_pool_*                  a host-side page allocator and the page
  *                                     tables it uploads.
  *
@@ -243,6 +250,69 @@ attn_status_t attn_prefill_paged(const void* q, const void* k_pool, const void* 
                                  int num_pages, int max_pages, int max_seq_len,
                                  float scale, int causal, int window,
                                  void* out, float* lse, attn_stream_t stream);
+
+/*
+ * attn_prefill_packed -- bf16 prefill of B sequences of different lengths whose
+ * tokens lie one after another, with no padding between them ("packed").
+ *
+ * q, out : [Tq, Hq,  D] bf16: token t, head h at element t * stride + h * D;
+ *          out must not overlap q, k or v
+ * k, v   : [Tk, Hkv, D] bf16, likewise
+ * q_stride, k_stride, v_stride, out_stride : elements from one token to the
+ *          next, multiples of 8, at least heads * D.  Slices of one fused
+ *          projection output (q, k, v of a token side by side) are taken as
+ *          they are.
+ * cu_seqlens_q : [B + 1] int32 (device), cumulative: sequence b's queries are
+ *          rows [cu_seqlens_q[b], cu_seqlens_q[b + 1]) of q and out
+ * cu_seqlens_k : [B + 1] int32 (device), the same for k and v (the same array
+ *          where every sequence attends to itself)
+ * lse    : [Tq, Hq] float or NULL (as attn_prefill_lse)
+ * D, scale, causal, window : as attn_prefill, per sequence: off is the
+ *          sequence's own number of keys minus its number of queries.
+ * B at most 65535; Tq and Tk at most 2^30 rows.
+ *
+ * A sequence may be empty on either side (a query without keys gives 0 and
+ * lse -inf).  Rows of out and lse that no sequence holds (before
+ * cu_seqlens_q[0], from cu_seqlens_q[B] on) are left as they were, so a
+ * buffer may be longer than the batch, and a captured graph replayed with
+ * other lengths up to Tq.  No sequence reads another's rows, nor rows behind
+ * the last, into its result, whatever they hold (NaN included); a NaN or
+ * infinity in a V row of the sequence itself may reach query rows of the same
+ * 128-key tile that do not see it (0 * NaN).  A cumulative length that
+ * decreases, is negative or passes Tq (Tk) is cut to the buffer and reported
+ * as ATTN_ERR_BAD_PAGE by attn_device_status.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
+ */
+attn_status_t attn_prefill_packed(const void* q, const void* k, const void* v,
+                                  const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                  int B, int Tq, int Tk, int Hq, int Hkv, int D,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
+                                  float scale, int causal, int window,
+                                  void* out, float* lse, attn_stream_t stream);
+
+/*
+ * attn_prefill_packed_paged -- attn_prefill_packed whose keys and values sit in
+ * the paged cache: the queries of sequence b are its newest
+ * cu_seqlens_q[b + 1] - cu_seqlens_q[b] tokens, a number of its own (prompts
+ * prefilled in chunks of what fits, sequences with nothing to do this time).
+ *
+ * q, out, lse, cu_seqlens_q, q_stride, out_stride, D, scale, causal, window :
+ *              as attn_prefill_packed
+ * k_pool, v_pool, page_table, seq_lens, page_size, num_pages, max_pages,
+ * max_seq_len : as attn_prefill_paged (seq_lens counts the new tokens, already
+ *              appended; max_seq_len at most 2^30), with its treatment of
+ *              slots behind the last token and of bad pages.
+ * For single tokens attn_decode_paged splits a long cache over the GPU; this
+ * call gives each (sequence, group of heads) to one SM.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
+ */
+attn_status_t attn_prefill_packed_paged(const void* q, const void* k_pool, const void* v_pool,
+                                        const int32_t* cu_seqlens_q, const int32_t* page_table,
+                                        const int32_t* seq_lens, int page_size, int B, int Tq, int Hq, int Hkv,
+                                        int D, int64_t q_stride, int64_t out_stride,
+                                        int num_pages, int max_pages, int max_seq_len,
+                                        float scale, int causal, int window,
+                                        void* out, float* lse, attn_stream_t stream);
 
 /*
  * attn_decode_paged -- one decode step for N sequences over a paged KV cache.
@@ -513,6 +583,68 @@ attn_status_t attn_kv_append_fp8(const void* k_new, const void* v_new, uint8_t* 
                                  int page_size, int B, int Hkv, int S_new, int D,
                                  int num_pages, int max_pages, float k_scale, float v_scale,
                                  attn_stream_t stream);
+
+/*
+ * attn_kv_append_rope -- rotate the q and k of new tokens by their positions and
+ * write k and v into the paged cache, in one pass.
+ *
+ * The tokens of B sequences are packed: sequence b's are rows
+ * [cu_seqlens[b], cu_seqlens[b + 1]), n of them, and the i-th sits at position
+ * p = seq_lens[b] - n + i of its cache (seq_lens: AFTER the append).  Every
+ * pair (a, b) of columns of a head of q and of k, c < rot_dim / 2, becomes
+ *     a * cos[p, c] - b * sin[p, c],   b * cos[p, c] + a * sin[p, c]
+ * in fp32, rounded once.  The pair is columns (c, c + rot_dim / 2), or
+ * (2c, 2c + 1) with interleaved = 1; columns from rot_dim on, and v, are kept.
+ *
+ * q     : [T, Hq, D] bf16 or NULL; q_out : the same shape, receives the rotated
+ *         q (NULL iff q is).  For one token per sequence it is the q of
+ *         attn_decode_paged.
+ * k, v  : [T, Hkv, D] bf16; k_out : [T, Hkv, D] bf16 or NULL, receives the
+ *         rotated k (for attn_prefill_packed)
+ * *_stride : elements from one token to the next of each, multiples of 8, at
+ *         least heads * D (ignored for a NULL buffer).  q_out may be q and k_out
+ *         may be k (same pointer and stride); no other two buffers overlap.
+ * k_pool, v_pool : [num_pages, Hkv, page_size, D] bf16, written in place
+ * cos_sin : [max_pos, rot_dim] float: row p holds the rot_dim / 2 cosines of
+ *         position p's angles, then their sines
+ * cu_seqlens : [B + 1] int32 (device), or NULL: T / B tokens of every sequence
+ *         (T a multiple of B; one decode step is T = B)
+ * page_table [B, max_pages], seq_lens [B], page_size (a multiple of 8) : as
+ *         attn_kv_append
+ * D a multiple of 16, at most 512; rot_dim a multiple of 16, 0 .. D (0: a plain
+ *         packed append, cos_sin may be NULL).
+ * Rows that no sequence holds, and tokens at positions below 0, are skipped:
+ * nothing is written for them.  A position from max_pos on is skipped and
+ * reported as ATTN_ERR_BAD_PAGE by attn_device_status; so is, for the pools
+ * alone, one that has no valid page.  Two tokens that land in the same slot
+ * (pages shared by sequences that both append to them) leave either's values.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
+ */
+attn_status_t attn_kv_append_rope(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                                  void* k_pool, void* v_pool, const float* cos_sin,
+                                  const int32_t* cu_seqlens, const int32_t* page_table,
+                                  const int32_t* seq_lens, int page_size, int B, int T, int Hq, int Hkv,
+                                  int D, int rot_dim, int interleaved,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                  int64_t q_out_stride, int64_t k_out_stride,
+                                  int num_pages, int max_pages, int max_pos, attn_stream_t stream);
+
+/*
+ * attn_kv_append_rope_fp8 -- attn_kv_append_rope into an 8-bit cache (the pools of
+ * attn_decode_paged_fp8): the fp32 value of each rotated k element, and each v
+ * element, becomes the E4M3 code nearest to it times 1 / k_scale (1 / v_scale),
+ * as attn_kv_append_fp8 encodes.  The rotated k is encoded from fp32, not from
+ * its bf16 rounding; q_out and k_out stay bf16.
+ */
+attn_status_t attn_kv_append_rope_fp8(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                                      uint8_t* k_pool, uint8_t* v_pool, const float* cos_sin,
+                                      const int32_t* cu_seqlens, const int32_t* page_table,
+                                      const int32_t* seq_lens, int page_size, int B, int T, int Hq, int Hkv,
+                                      int D, int rot_dim, int interleaved,
+                                      int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                      int64_t q_out_stride, int64_t k_out_stride,
+                                      int num_pages, int max_pages, int max_pos,
+                                      float k_scale, float v_scale, attn_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,6 +14,7 @@ ATTN_STATUS = {
 
 # name -> (restype, argtypes); mirrors include/attn_b200.h
 _c_int, _c_float, _c_size, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+_c_i64 = ctypes.c_int64
 PROTOTYPES = {
     "attn_status_string": (ctypes.c_char_p, [_c_int]),
     "attn_version": (_c_int, []),
@@ -33,6 +34,12 @@ PROTOTYPES = {
     "attn_selftest_wait_timeout": (_c_int, [_c_int, _vp]),
     "attn_kv_append": (_c_int, [_vp] * 6 + [_c_int] * 7 + [_vp]),
     "attn_kv_append_fp8": (_c_int, [_vp] * 6 + [_c_int] * 7 + [_c_float, _c_float, _vp]),
+    "attn_prefill_packed": (_c_int, [_vp] * 5 + [_c_int] * 6 + [_c_i64] * 4 + [_c_float, _c_int, _c_int, _vp, _vp, _vp]),
+    "attn_prefill_packed_paged": (_c_int, [_vp] * 6 + [_c_int] * 6 + [_c_i64] * 2 + [_c_int] * 3
+                                  + [_c_float, _c_int, _c_int, _vp, _vp, _vp]),
+    "attn_kv_append_rope": (_c_int, [_vp] * 11 + [_c_int] * 8 + [_c_i64] * 5 + [_c_int] * 3 + [_vp]),
+    "attn_kv_append_rope_fp8": (_c_int, [_vp] * 11 + [_c_int] * 8 + [_c_i64] * 5 + [_c_int] * 3
+                                + [_c_float, _c_float, _vp]),
     "attn_page_pool_create": (_c_int, [_c_int] * 4 + [ctypes.POINTER(_vp)]),
     "attn_page_pool_destroy": (None, [_vp]),
     "attn_page_pool_resize": (_c_int, [_vp, _c_int, _c_int]),

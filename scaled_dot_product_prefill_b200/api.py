@@ -17,6 +17,7 @@ __all__ = ["attn_prefill", "attn_prefill_f32", "attn_prefill_lse", "attn_prefill
            "attn_prefill_paged", "attn_prefill_host", "attn_decode_paged", "attn_decode_paged_noalloc",
            "attn_decode_step_host",
            "attn_decode_paged_workspace_size", "attn_decode_paged_fp8", "attn_kv_append", "attn_kv_append_fp8",
+           "attn_prefill_packed", "attn_prefill_packed_paged", "attn_kv_append_rope", "attn_kv_append_rope_fp8",
            "PagePool",
            "attn_device_status", "attn_selftest_wait_timeout", "attn_status_string", "attn_version", "AttnError"]
 
@@ -455,6 +456,224 @@ def attn_kv_append_fp8(k_new, v_new, k_pool, v_pool, page_table, seq_lens, *, k_
     _check("attn_kv_append_fp8", _lib.load().attn_kv_append_fp8(
         _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(page_table), _ptr(seq_lens), page_size, B, Hkv,
         S_new, D, num_pages, page_table.shape[1], float(k_scale), float(v_scale), _stream(stream)))
+
+
+def _packed(t, name, heads, D, like=None):
+    """Token stride of a packed [T, heads, D] bf16 tensor (any stride between tokens, heads side by side)."""
+    if t.dim() != 3 or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bfloat16 [tokens, heads, D] tensor, got {t.dtype} {tuple(t.shape)}")
+    T, H, d = t.shape
+    if H != heads or d != D or (like is not None and T != like):
+        raise ValueError(f"{name} must have shape {(T if like is None else like, heads, D)}, got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    row = heads * D
+    if T <= 1:
+        s0 = row if s0 < row or s0 % 8 else s0
+    if T and row and ((s2 != 1 and D > 1) or (s1 != D and heads > 1) or s0 < row or s0 % 8):
+        raise ValueError(f"{name} must have its heads contiguous and a token stride that is a multiple of 8 and at "
+                         f"least {row}, got strides {(s0, s1, s2)}")
+    return s0 if row else 0
+
+
+def _on_device(*named):
+    """Every (tensor, name) lies on the current CUDA device; contiguity is the caller's matter."""
+    dev = None
+    for t, name in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor on the current device")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+
+
+def _int32(t, name, shape):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _contiguous(t, name, shape, dtype):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _made_here(stream, *ts):
+    """Tensors allocated on the current stream for a call on another one: kept from early reuse."""
+    if stream is not None and stream != torch.cuda.current_stream():
+        for t in ts:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _cuda_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _batch_of(cu, name):
+    if cu.dim() != 1 or cu.shape[0] < 1:
+        raise ValueError(f"{name} must have shape [B + 1], got {tuple(cu.shape)}")
+    return cu.shape[0] - 1
+
+
+def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True, window=0, scale=None, out=None,
+                        lse=None, want_lse=False, stream=None):
+    """bf16 prefill of sequences of different lengths, packed: q [Tq,Hq,D], k/v [Tk,Hkv,D] -> out [Tq,Hq,D].
+
+    Sequence b holds rows cu_seqlens_q[b]:cu_seqlens_q[b+1] of q and out, and
+    cu_seqlens_k[b]:cu_seqlens_k[b+1] of k and v (default: the same).  The cumulative
+    lengths are int32 [B+1] CUDA tensors.  q, k, v and out may have any token stride that is
+    a multiple of 8 (slices of a fused projection).  Rows that no sequence holds are left
+    as they were.  Returns out, or (out, lse) with want_lse (or an lse tensor given); lse [Tq,Hq] fp32.
+    """
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, D]")
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    q_stride = _packed(q, "q", Hq, D)
+    k_stride = _packed(k, "k", Hkv, D)
+    v_stride = _packed(v, "v", Hkv, D, like=Tk)
+    B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
+    if cu_seqlens_k is None:
+        if Tk != Tq:
+            raise ValueError(f"without cu_seqlens_k, k and v must have q's {Tq} rows, got {Tk}")
+        cu_seqlens_k = cu_seqlens_q
+    cu_q = _int32(cu_seqlens_q, "cu_seqlens_q", (B + 1,))
+    cu_k = _int32(cu_seqlens_k, "cu_seqlens_k", (B + 1,))
+    made = []
+    if out is None:
+        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
+        made.append(out)
+    if lse is None and want_lse:
+        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+        made.append(lse)
+    out_stride = _packed(out, "out", Hq, D, like=Tq)
+    lse_ptr = None if lse is None else _contiguous(lse, "lse", (Tq, Hq), torch.float32)
+    _on_device((q, "q"), (k, "k"), (v, "v"), (cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k"),
+               (out, "out"), (lse, "lse"))
+    _made_here(stream, *made)
+    _check("attn_prefill_packed", _lib.load().attn_prefill_packed(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
+        out_stride, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)), int(window),
+        out.data_ptr(), lse_ptr, _cuda_stream(stream)))
+    return out if lse is None else (out, lse)
+
+
+def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, *, max_seq_len, causal=True,
+                              window=0, scale=None, out=None, lse=None, want_lse=False, stream=None):
+    """Chunked prefill of packed queries over the paged cache: q [Tq,Hq,D], each sequence its own number of rows.
+
+    Rows cu_seqlens_q[b]:cu_seqlens_q[b+1] are the newest tokens of sequence b, whose cache (pools
+    [num_pages,Hkv,page_size,D], page_table [B,max_pages], seq_lens [B]) already holds them.
+    Strides, rows of no sequence and the result are as attn_prefill_packed's.
+    """
+    if q.dim() != 3 or k_pool.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("q must be [tokens,Hq,D], the pools [num_pages,Hkv,page_size,D], page_table [B,max_pages]")
+    Tq, Hq, D = q.shape
+    num_pages, Hkv, page_size, _ = k_pool.shape
+    q_stride = _packed(q, "q", Hq, D)
+    B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
+    max_pages = page_table.shape[1]
+    pool = (num_pages, Hkv, page_size, D)
+    kp = _contiguous(k_pool, "k_pool", pool, torch.bfloat16)
+    vp = _contiguous(v_pool, "v_pool", pool, torch.bfloat16)
+    cu_q = _int32(cu_seqlens_q, "cu_seqlens_q", (B + 1,))
+    table = _int32(page_table, "page_table", (B, max_pages))
+    lens = _int32(seq_lens, "seq_lens", (B,))
+    made = []
+    if out is None:
+        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
+        made.append(out)
+    if lse is None and want_lse:
+        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+        made.append(lse)
+    out_stride = _packed(out, "out", Hq, D, like=Tq)
+    lse_ptr = None if lse is None else _contiguous(lse, "lse", (Tq, Hq), torch.float32)
+    _on_device((q, "q"), (k_pool, "k_pool"), (v_pool, "v_pool"), (cu_seqlens_q, "cu_seqlens_q"),
+               (page_table, "page_table"), (seq_lens, "seq_lens"), (out, "out"), (lse, "lse"))
+    _made_here(stream, *made)
+    _check("attn_prefill_packed_paged", _lib.load().attn_prefill_packed_paged(
+        q.data_ptr(), kp, vp, cu_q, table, lens, page_size, B, Tq, Hq, Hkv, D, q_stride, out_stride, num_pages,
+        max_pages, int(max_seq_len), 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)),
+        int(window), out.data_ptr(), lse_ptr, _cuda_stream(stream)))
+    return out if lse is None else (out, lse)
+
+
+def _append_rope(name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens, interleaved,
+                 q_out, k_out, stream, scales):
+    if k.dim() != 3 or k_pool.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k and v must be [tokens,Hkv,D], the pools [num_pages,Hkv,page_size,D], page_table "
+                         "[B,max_pages]")
+    T, Hkv, D = k.shape
+    num_pages, _, page_size, _ = k_pool.shape
+    B, max_pages = page_table.shape
+    k_stride, v_stride = _packed(k, "k", Hkv, D), _packed(v, "v", Hkv, D, like=T)
+    Hq = q_stride = q_out_stride = k_out_stride = 0
+    made = []
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, Hq, D]")
+        Hq = q.shape[1]
+        q_stride = _packed(q, "q", Hq, D, like=T)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+            made.append(q_out)
+        q_out_stride = _packed(q_out, "q_out", Hq, D, like=T)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if k_out is not None:
+        k_out_stride = _packed(k_out, "k_out", Hkv, D, like=T)
+    pool = (num_pages, Hkv, page_size, D)
+    kp, vp = _contiguous(k_pool, "k_pool", pool, pool_dtype), _contiguous(v_pool, "v_pool", pool, pool_dtype)
+    max_pos = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 [max_pos, rot_dim] tensor")
+        max_pos, rot = cos_sin.shape
+        if rot > D:
+            raise ValueError(f"cos_sin must have at most {D} columns, got {rot}")
+    table = _int32(page_table, "page_table", (B, max_pages))
+    lens = _int32(seq_lens, "seq_lens", (B,))
+    cu = None
+    if cu_seqlens is not None:
+        cu = _int32(cu_seqlens, "cu_seqlens", (B + 1,))
+    elif B and T % B:
+        raise ValueError(f"without cu_seqlens the {T} tokens must be the same number of each of {B} sequences")
+    _on_device((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"), (k_out, "k_out"), (k_pool, "k_pool"),
+               (v_pool, "v_pool"), (cos_sin, "cos_sin"), (page_table, "page_table"), (seq_lens, "seq_lens"),
+               (cu_seqlens, "cu_seqlens"))
+    _made_here(stream, *made)
+    _check(name, getattr(_lib.load(), name)(
+        None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), None if q is None else q_out.data_ptr(),
+        None if k_out is None else k_out.data_ptr(), kp, vp, None if cos_sin is None else cos_sin.data_ptr(), cu, table,
+        lens, page_size, B, T, Hq, Hkv, D, rot, int(bool(interleaved)), q_stride, k_stride, v_stride, q_out_stride,
+        k_out_stride, num_pages, max_pages, max_pos, *scales, _cuda_stream(stream)))
+    return q_out
+
+
+def attn_kv_append_rope(q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, *, cu_seqlens=None, interleaved=False,
+                        q_out=None, k_out=None, stream=None):
+    """Rotate packed q [T,Hq,D] and k [T,Hkv,D] by position and write k and v into the paged cache; returns q_out.
+
+    Rows cu_seqlens[b]:cu_seqlens[b+1] are the newest tokens of sequence b (None: T / B of every
+    sequence; T = B is one decode step, whose q_out is attn_decode_paged's q), at the last
+    positions of its cache of seq_lens[b] tokens.  cos_sin [max_pos, rot_dim] fp32 holds the
+    cosines, then the sines, of each position's angles; rot_dim <= D columns turn (None: none), in
+    pairs (c, c + rot_dim / 2), or (2c, 2c + 1) if interleaved.  q may be None; q_out may be q;
+    k_out (optional, may be k) receives the rotated k.  Strides as attn_prefill_packed.
+    """
+    return _append_rope("attn_kv_append_rope", torch.bfloat16, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens,
+                        cu_seqlens, interleaved, q_out, k_out, stream, ())
+
+
+def attn_kv_append_rope_fp8(q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, *, k_scale, v_scale,
+                            cu_seqlens=None, interleaved=False, q_out=None, k_out=None, stream=None):
+    """attn_kv_append_rope into uint8 E4M3 pools: code = nearest E4M3 to the fp32 value * (1/scale), ties to even."""
+    return _append_rope("attn_kv_append_rope_fp8", torch.uint8, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens,
+                        cu_seqlens, interleaved, q_out, k_out, stream, (float(k_scale), float(v_scale)))
 
 
 class PagePool:

@@ -92,7 +92,7 @@ const char* attn_status_string(attn_status_t s) {
   return "ATTN_ERR_UNKNOWN";
 }
 
-int attn_version(void) { return 103; }
+int attn_version(void) { return 104; }
 
 }  // extern "C"
 
@@ -178,6 +178,91 @@ attn_status_t attn_prefill_paged(const void* q, const void* k_pool, const void* 
   return from_cuda(attn::launch_prefill_tc_paged(q, k_pool, v_pool, page_table, seq_lens, page_size, B, Hq, Hkv, Sq,
                                                  D, num_pages, max_pages, max_seq_len, scale, causal, window, out, lse,
                                                  attn::device_error_word(), s));
+}
+
+namespace {
+
+// A packed [tokens, heads, D] buffer's distance between tokens: whole 16-byte pieces, rows that do not
+// overlap, within what a tensor map takes.
+bool good_stride(int64_t stride, int heads, int D) {
+  return stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * D && stride < (1LL << 38);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// What the packed prefills check alike; ATTN_OK also for an empty batch (B, Tq or Hq 0).
+attn_status_t check_packed(const void* q, const int32_t* cu_q, const void* out, const float* lse, int B, int Tq,
+                           int Hq, int Hkv, int D, int64_t q_stride, int64_t out_stride, float scale, int causal,
+                           int window) {
+  if (B < 0 || Tq < 0 || Hq < 0 || Hkv < 0 || D <= 0 || window < 0) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || Tq == 0 || Hq == 0) return ATTN_OK;
+  if (Hkv == 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (q == nullptr || out == nullptr || cu_q == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned4(cu_q) || !aligned4(lse)) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_INVALID_ARG;
+  if (!good_stride(q_stride, Hq, D) || !good_stride(out_stride, Hq, D)) return ATTN_ERR_INVALID_ARG;
+  if (window > 0 && !causal) return ATTN_ERR_UNSUPPORTED;
+  // positions and key indices are int32 with room for a window below and a tile above
+  if (Tq > (1 << 30) || B > 65535) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+attn_status_t from_packed(cudaError_t e) {
+  if (e == cudaErrorNotSupported) return ATTN_ERR_UNSUPPORTED;   // more work items than the kernel counts
+  return from_cuda(e);
+}
+
+// A window this long hides nothing that int32 positions can hold.
+int cut_window(int window) { return window < (1 << 30) ? window : (1 << 30); }
+
+}  // namespace
+
+attn_status_t attn_prefill_packed(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                                  const int32_t* cu_seqlens_k, int B, int Tq, int Tk, int Hq, int Hkv, int D,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
+                                  float scale, int causal, int window, void* out, float* lse, attn_stream_t stream) {
+  const attn_status_t st =
+      check_packed(q, cu_seqlens_q, out, lse, B, Tq, Hq, Hkv, D, q_stride, out_stride, scale, causal, window);
+  if (st != ATTN_OK || B == 0 || Tq == 0 || Hq == 0) return Tk < 0 ? ATTN_ERR_INVALID_ARG : st;
+  if (Tk < 0 || cu_seqlens_k == nullptr || !aligned4(cu_seqlens_k)) return ATTN_ERR_INVALID_ARG;
+  // without keys k and v are never read and may be null
+  if (Tk > 0 && (k == nullptr || v == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID_ARG;
+  if (!good_stride(k_stride, Hkv, D) || !good_stride(v_stride, Hkv, D)) return ATTN_ERR_INVALID_ARG;
+  if (Tk > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  return from_packed(attn::launch_prefill_tc_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, B, Tq, Tk, Hq, Hkv, D,
+                                                    q_stride, k_stride, v_stride, out_stride, scale, causal,
+                                                    cut_window(window), out, lse, attn::device_error_word(),
+                                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+attn_status_t attn_prefill_packed_paged(const void* q, const void* k_pool, const void* v_pool,
+                                        const int32_t* cu_seqlens_q, const int32_t* page_table,
+                                        const int32_t* seq_lens, int page_size, int B, int Tq, int Hq, int Hkv, int D,
+                                        int64_t q_stride, int64_t out_stride, int num_pages, int max_pages,
+                                        int max_seq_len, float scale, int causal, int window, void* out, float* lse,
+                                        attn_stream_t stream) {
+  const attn_status_t st =
+      check_packed(q, cu_seqlens_q, out, lse, B, Tq, Hq, Hkv, D, q_stride, out_stride, scale, causal, window);
+  if (num_pages < 0 || max_pages < 0 || max_seq_len < 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+  if (st != ATTN_OK || B == 0 || Tq == 0 || Hq == 0) return st;
+  if (seq_lens == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (max_seq_len > 0 && (k_pool == nullptr || v_pool == nullptr || page_table == nullptr || max_pages == 0 ||
+                          num_pages == 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned4(page_table) || !aligned4(seq_lens))
+    return ATTN_ERR_INVALID_ARG;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
+    return ATTN_ERR_UNSUPPORTED;
+  if (max_seq_len > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  // TMA plane coordinates (page * Hkv + g, one page past the pool for boxes past a sequence end) are int32
+  if ((static_cast<long long>(num_pages) + 1) * Hkv > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
+  return from_packed(attn::launch_prefill_tc_packed_paged(
+      q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, page_size, B, Tq, Hq, Hkv, D, q_stride, out_stride,
+      num_pages, max_pages, max_seq_len, scale, causal, cut_window(window), out, lse, attn::device_error_word(),
+      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // attn_prefill from and to host memory.  The work is cut into pieces of
@@ -443,6 +528,76 @@ attn_status_t attn_kv_append_fp8(const void* k_new, const void* v_new, uint8_t* 
                                  attn_stream_t stream) {
   return kv_append(k_new, v_new, k_pool, v_pool, page_table, seq_lens, page_size, B, Hkv, S_new, D, num_pages,
                    max_pages, stream, true, k_scale, v_scale);
+}
+
+}  // extern "C"
+
+namespace {
+
+attn_status_t kv_append_rope(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pool,
+                             void* v_pool, const float* cos_sin, const int32_t* cu_seqlens, const int32_t* page_table,
+                             const int32_t* seq_lens, int page_size, int B, int T, int Hq, int Hkv, int D, int rot_dim,
+                             int interleaved, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             int64_t q_out_stride, int64_t k_out_stride, int num_pages, int max_pages, int max_pos,
+                             attn_stream_t stream, bool fp8, float k_scale, float v_scale) {
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 0 || D <= 0 || rot_dim < 0 || rot_dim > D || page_size <= 0 || num_pages < 0 ||
+      max_pages < 0 || max_pos < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return ATTN_ERR_INVALID_ARG;
+  if (!(k_scale > 0.f) || !std::isfinite(k_scale) || !(v_scale > 0.f) || !std::isfinite(v_scale))
+    return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || T == 0 || Hkv == 0) return ATTN_OK;
+  if ((q == nullptr) != (q_out == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (q == nullptr) Hq = 0;   // only k and v
+  if (k == nullptr || v == nullptr || k_pool == nullptr || v_pool == nullptr || page_table == nullptr ||
+      seq_lens == nullptr || num_pages == 0 || max_pages == 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (cos_sin == nullptr || max_pos == 0)) return ATTN_ERR_INVALID_ARG;
+  if (cu_seqlens == nullptr && T % B != 0) return ATTN_ERR_INVALID_ARG;   // the same number of every sequence
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(cos_sin) || !aligned4(cu_seqlens) ||
+      !aligned4(page_table) || !aligned4(seq_lens))
+    return ATTN_ERR_INVALID_ARG;
+  if ((Hq > 0 && (!good_stride(q_stride, Hq, D) || !good_stride(q_out_stride, Hq, D))) ||
+      !good_stride(k_stride, Hkv, D) || !good_stride(v_stride, Hkv, D) ||
+      (k_out != nullptr && !good_stride(k_out_stride, Hkv, D)))
+    return ATTN_ERR_INVALID_ARG;
+  // in place means row for row
+  if ((Hq > 0 && q_out == q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride))
+    return ATTN_ERR_INVALID_ARG;
+  if (D % 16 != 0 || D > 512 || rot_dim % 16 != 0 || page_size % 8 != 0) return ATTN_ERR_UNSUPPORTED;
+  if (rot_dim == 0) max_pos = 0x7FFFFFFF;   // no angles to run out of
+  return from_cuda(attn::launch_kv_append_rope(
+      q, k, v, q_out, k_out, k_pool, v_pool, cos_sin, cu_seqlens, page_table, seq_lens, page_size, B, T, Hq, Hkv, D,
+      rot_dim, interleaved, q_stride, k_stride, v_stride, q_out_stride, k_out_stride, num_pages, max_pages, max_pos,
+      attn::device_error_word(), reinterpret_cast<cudaStream_t>(stream), fp8, k_scale, v_scale));
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_kv_append_rope(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pool,
+                                  void* v_pool, const float* cos_sin, const int32_t* cu_seqlens,
+                                  const int32_t* page_table, const int32_t* seq_lens, int page_size, int B, int T,
+                                  int Hq, int Hkv, int D, int rot_dim, int interleaved, int64_t q_stride,
+                                  int64_t k_stride, int64_t v_stride, int64_t q_out_stride, int64_t k_out_stride,
+                                  int num_pages, int max_pages, int max_pos, attn_stream_t stream) {
+  return kv_append_rope(q, k, v, q_out, k_out, k_pool, v_pool, cos_sin, cu_seqlens, page_table, seq_lens, page_size, B,
+                        T, Hq, Hkv, D, rot_dim, interleaved, q_stride, k_stride, v_stride, q_out_stride, k_out_stride,
+                        num_pages, max_pages, max_pos, stream, false, 1.f, 1.f);
+}
+
+attn_status_t attn_kv_append_rope_fp8(const void* q, const void* k, const void* v, void* q_out, void* k_out,
+                                      uint8_t* k_pool, uint8_t* v_pool, const float* cos_sin,
+                                      const int32_t* cu_seqlens, const int32_t* page_table, const int32_t* seq_lens,
+                                      int page_size, int B, int T, int Hq, int Hkv, int D, int rot_dim,
+                                      int interleaved, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                      int64_t q_out_stride, int64_t k_out_stride, int num_pages, int max_pages,
+                                      int max_pos, float k_scale, float v_scale, attn_stream_t stream) {
+  return kv_append_rope(q, k, v, q_out, k_out, k_pool, v_pool, cos_sin, cu_seqlens, page_table, seq_lens, page_size, B,
+                        T, Hq, Hkv, D, rot_dim, interleaved, q_stride, k_stride, v_stride, q_out_stride, k_out_stride,
+                        num_pages, max_pages, max_pos, stream, true, k_scale, v_scale);
 }
 
 }  // extern "C"

@@ -75,6 +75,18 @@ cudaError_t launch_prefill_tc_paged(const void* q, const void* k_pool, const voi
                                     const int32_t* seq_lens, int page_size, int B, int Hq, int Hkv, int Sq, int D,
                                     int num_pages, int max_pages, int max_seq_len, float scale, int causal,
                                     int window, void* out, float* lse, unsigned int* err, cudaStream_t stream);
+// Packed sequences: q/out [Tq, Hq, D], k/v [Tk, Hkv, D] with token strides in elements, cumulative
+// lengths cu_q, cu_k [B + 1] on the device; lse (optional) [Tq, Hq].
+cudaError_t launch_prefill_tc_packed(const void* q, const void* k, const void* v, const int32_t* cu_q,
+                                     const int32_t* cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int D,
+                                     long long q_stride, long long k_stride, long long v_stride, long long out_stride,
+                                     float scale, int causal, int window, void* out, float* lse, unsigned int* err,
+                                     cudaStream_t stream);
+cudaError_t launch_prefill_tc_packed_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* cu_q,
+                                           const int32_t* page_table, const int32_t* seq_lens, int page_size, int B,
+                                           int Tq, int Hq, int Hkv, int D, long long q_stride, long long out_stride,
+                                           int num_pages, int max_pages, int max_seq_len, float scale, int causal,
+                                           int window, void* out, float* lse, unsigned int* err, cudaStream_t stream);
 cudaError_t launch_prefill_f32(const float* q, const float* k, const float* v, float* out, float* lse, int B,
                                int Hq, int Hkv, int Sq, int Skv, int D, float scale, int causal, int window,
                                cudaStream_t stream);
@@ -98,5 +110,15 @@ cudaError_t launch_kv_append(const void* k_new, const void* v_new, void* k_pool,
                              const int32_t* page_table, const int32_t* seq_lens, int page_size, int B, int Hkv,
                              int S_new, int D, int num_pages, int max_pages, unsigned int* err, cudaStream_t stream,
                              bool fp8 = false, float k_scale = 1.f, float v_scale = 1.f);
+
+// Packed rows q [T, Hq, D], k/v [T, Hkv, D]: q and k rotated by position (R of D columns; table [max_pos, R]
+// fp32), k and v stored in the pools; q_out, k_out optional.  cu_seqlens null: T / B rows of every sequence.
+cudaError_t launch_kv_append_rope(const void* q, const void* k, const void* v, void* q_out, void* k_out, void* k_pool,
+                                  void* v_pool, const float* table, const int32_t* cu_seqlens,
+                                  const int32_t* page_table, const int32_t* seq_lens, int page_size, int B, int T,
+                                  int Hq, int Hkv, int D, int R, int interleaved, long long q_stride,
+                                  long long k_stride, long long v_stride, long long q_out_stride,
+                                  long long k_out_stride, int num_pages, int max_pages, int max_pos, unsigned int* err,
+                                  cudaStream_t stream, bool fp8, float k_scale, float v_scale);
 
 }  // namespace attn

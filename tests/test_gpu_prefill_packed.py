@@ -1,0 +1,340 @@
+"""GPU tests of the packed prefills: sequences of different lengths, dense and over the paged cache."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import sdpa
+from packed_oracle import assert_packed, cumulative, f64, packed_attention
+from scaled_dot_product_prefill_b200 import api, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+def run_packed(q, k, v, cu_q, cu_k=None, **kw):
+    api.attn_device_status(clear=True)
+    got = api.attn_prefill_packed(q.cuda(), k.cuda(), v.cuda(), cu_q.cuda(), None if cu_k is None else cu_k.cuda(),
+                                  want_lse=True, **kw)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 0
+    return got
+
+
+def tensors(Tq, Tk, Hq, Hkv, D, seed):
+    return (inputs.normal((Tq, Hq, D), seed), inputs.normal((Tk, Hkv, D), seed + 1),
+            inputs.normal((Tk, Hkv, D), seed + 2))
+
+
+SELF = [
+    # Hq, Hkv, D, lengths, causal, window
+    (4, 4, 64, [1], True, 0),
+    (8, 2, 128, [1], True, 0),
+    (8, 2, 128, [1, 1, 1, 1, 1], True, 0),
+    (4, 4, 64, [0, 5, 0, 130, 128, 127, 129, 0], True, 0),
+    (8, 2, 128, [0, 5, 0, 130, 128, 127, 129, 0], True, 0),
+    (8, 1, 128, [256, 255, 257, 33, 31, 32], True, 0),
+    (8, 1, 64, [17, 300, 16, 15], True, 0),
+    (12, 4, 128, [100, 260], True, 0),           # groups of 3: no shared tiles
+    (6, 1, 64, [90, 1, 200], True, 0),           # groups of 6: pairs of heads share a tile
+    (5, 5, 128, [140], True, 0),
+    (16, 1, 128, [70, 20], True, 0),
+    (32, 1, 64, [40, 5], True, 0),
+    (128, 1, 64, [3, 6], True, 0),               # a tile is one token
+    (8, 2, 64, [400, 130], True, 1),             # a window of the token itself
+    (8, 2, 128, [400, 130], True, 7),
+    (4, 1, 128, [700, 10], True, 128),
+    (4, 2, 64, [513, 300], True, 200),
+    (4, 2, 128, [300, 20], True, 2 ** 31 - 1),   # a window longer than anything
+    (8, 2, 128, [200, 0, 77, 1], False, 0),
+    (4, 4, 64, [128, 129, 300], False, 0),
+]
+
+
+@pytest.mark.parametrize("case", SELF, ids=[str(c) for c in SELF])
+def test_packed_prefill_matches_the_definition(case):
+    Hq, Hkv, D, lens, causal, window = case
+    T = sum(lens)
+    q, k, v = tensors(T, T, Hq, Hkv, D, seed=T + Hq)
+    cu = cumulative(lens)
+    got = run_packed(q, k, v, cu, causal=causal, window=window)
+    assert_packed(got, packed_attention(f64(q), f64(k), f64(v), cu.tolist(), cu.tolist(), D ** -0.5, causal, window),
+                  str(case))
+
+
+CROSS = [
+    # Hq, Hkv, D, query lengths, key lengths, causal, window
+    (8, 2, 128, [5, 130, 1], [300, 130, 513], True, 0),
+    (8, 2, 64, [300, 40, 129], [10, 0, 128], True, 0),        # rows that see nothing, a sequence without keys
+    (4, 4, 128, [0, 300, 7], [50, 20, 0], True, 0),           # a sequence without queries
+    (4, 1, 128, [60, 200], [1000, 900], True, 130),
+    (4, 2, 64, [200, 3], [150, 70], True, 5),
+    (4, 2, 128, [33, 150, 9], [200, 0, 129], False, 0),
+    (6, 2, 64, [200], [1], True, 0),
+]
+
+
+@pytest.mark.parametrize("case", CROSS, ids=[str(c) for c in CROSS])
+def test_queries_and_keys_of_different_lengths(case):
+    Hq, Hkv, D, lq, lk, causal, window = case
+    q, k, v = tensors(sum(lq), sum(lk), Hq, Hkv, D, seed=7 + sum(lk))
+    cu_q, cu_k = cumulative(lq), cumulative(lk)
+    got = run_packed(q, k, v, cu_q, cu_k, causal=causal, window=window, scale=0.11)
+    assert_packed(got, packed_attention(f64(q), f64(k), f64(v), cu_q.tolist(), cu_k.tolist(), 0.11, causal, window),
+                  str(case))
+
+
+def test_no_keys_at_all():
+    q, _, _ = tensors(40, 0, 4, 2, 64, 3)
+    kv = torch.empty((0, 2, 64), dtype=torch.bfloat16)
+    out, lse = run_packed(q, kv, kv, cumulative([30, 10]), cumulative([0, 0]))
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("D,window", [(64, 0), (128, 0), (128, 150)])
+def test_many_sequences_more_items_than_sms(D, window):
+    r = np.random.default_rng(4)
+    lens = r.integers(0, 300, 70).tolist()
+    T = sum(lens)
+    q, k, v = tensors(T, T, 8, 4, D, seed=11)
+    cu = cumulative(lens)
+    got = run_packed(q, k, v, cu, window=window)
+    assert_packed(got, packed_attention(f64(q), f64(k), f64(v), cu.tolist(), cu.tolist(), D ** -0.5, True, window))
+    # each sequence alone gives the same bits: nothing depends on its neighbours or its place
+    for b in (0, 13, 69):
+        a, e = int(cu[b]), int(cu[b + 1])
+        if a == e:
+            continue
+        one = api.attn_prefill_packed(q[a:e].cuda(), k[a:e].cuda(), v[a:e].cuda(), cumulative([e - a]).cuda(),
+                                      window=window)
+        assert torch.equal(one, got[0][a:e])
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,causal,window", [(64, 4, 4, True, 0), (128, 8, 2, True, 0), (128, 8, 2, True, 300),
+                                                    (64, 4, 1, False, 0)])
+def test_equal_lengths_give_the_bits_of_the_dense_prefill(D, Hq, Hkv, causal, window):
+    B, S = 3, 777
+    p = inputs.prefill_inputs(B, Hq, Hkv, S, S, D, seed=8)
+    dense, dense_lse = api.attn_prefill_lse(p.q.cuda(), p.k.cuda(), p.v.cuda(), causal=causal, window=window)
+    rows = lambda x: x.transpose(1, 2).reshape(B * S, x.shape[1], D).contiguous()  # noqa: E731
+    out, lse = run_packed(rows(p.q), rows(p.k), rows(p.v), cumulative([S] * B), causal=causal, window=window)
+    assert torch.equal(out.view(B, S, Hq, D).transpose(1, 2), dense)
+    assert torch.equal(lse.view(B, S, Hq).transpose(1, 2), dense_lse)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_what_lies_around_a_sequence_never_reaches_it(D):
+    """NaN before the first sequence, in the middle one and behind the last: the others keep their bits, the rows of no
+    sequence keep what they held."""
+    Hq, Hkv, lens, front, back = 8, 2, [75, 140, 130, 1, 60], 9, 200
+    T = front + sum(lens) + back
+    q, k, v = tensors(T, T, Hq, Hkv, D, seed=21)
+    cu = cumulative(lens, front)
+    clean = run_packed(q, k, v, cu)
+    mine = torch.zeros(T, dtype=torch.bool)
+    for b in (0, 2, 3, 4):
+        mine[int(cu[b]):int(cu[b + 1])] = True
+    for x in (q, k, v):
+        x[~mine] = float("nan")
+        x[int(cu[1]):int(cu[2])][::3] = float("inf")
+    out = torch.full((T, Hq, D), 3.5, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hq), -7.25, device="cuda")
+    run_packed(q, k, v, cu, out=out, lse=lse)
+    assert torch.equal(out[mine.cuda()], clean[0][mine.cuda()])
+    assert torch.equal(lse[mine.cuda()], clean[1][mine.cuda()])
+    for edge in (slice(0, front), slice(T - back, T)):
+        assert (out[edge] == 3.5).all() and (lse[edge] == -7.25).all()
+
+
+def test_masked_keys_with_nan_scores_are_never_seen():
+    """NaN and infinities in K rows that a query does not see stay out of it (V finite there)."""
+    q, k, v = tensors(300, 300, 4, 2, 128, 31)
+    cu = cumulative([300])
+    clean = run_packed(q, k, v, cu)
+    k[200:] = float("nan")
+    k[250:] = float("inf")
+    out, lse = run_packed(q, k, v, cu)
+    assert torch.equal(out[:200], clean[0][:200]) and torch.equal(lse[:200], clean[1][:200])
+
+
+def test_slices_of_a_fused_projection_and_a_strided_output():
+    Hq, Hkv, D, lens = 8, 2, 128, [33, 190, 64]
+    T = sum(lens)
+    qkv = inputs.normal((T, (Hq + 2 * Hkv) * D + 40), 5).cuda()
+    cut = lambda a, h: qkv[:, a:a + h * D].view(T, h, D)  # noqa: E731
+    q, k, v = cut(0, Hq), cut(Hq * D, Hkv), cut((Hq + Hkv) * D, Hkv)
+    wide = torch.full((T, Hq * D + 24), 2.0, dtype=torch.bfloat16, device="cuda")
+    out = wide[:, 8:8 + Hq * D].view(T, Hq, D)
+    cu = cumulative(lens).cuda()
+    api.attn_prefill_packed(q, k, v, cu, out=out)
+    want = api.attn_prefill_packed(q.contiguous(), k.contiguous(), v.contiguous(), cu)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert (wide[:, :8] == 2).all() and (wide[:, 8 + Hq * D:] == 2).all()
+
+
+def test_scores_far_apart_and_large():
+    """Scores of thousands: the reference maximum moves by far more than the exponent's range."""
+    Hq, Hkv, D, lens = 4, 2, 64, [150, 300]
+    T = sum(lens)
+    q, k, v = tensors(T, T, Hq, Hkv, D, 41)
+    q, k = q * 32, k * 32
+    cu = cumulative(lens)
+    got = run_packed(q, k, v, cu)
+    assert_packed(got, packed_attention(f64(q), f64(k), f64(v), cu.tolist(), cu.tolist(), D ** -0.5))
+
+
+PAGED = [
+    # Hq, Hkv, D, page, new tokens, cached tokens (new ones included), causal, window
+    (8, 2, 128, 16, [77, 1, 0, 300], [77, 300, 40, 1000], True, 0),
+    (4, 4, 64, 32, [256, 5, 1], [256, 700, 1], True, 0),
+    (8, 1, 128, 64, [130, 20], [40, 513], True, 0),            # a cache shorter than the chunk
+    (8, 2, 64, 128, [300, 64], [1500, 300], True, 200),
+    (4, 2, 128, 256, [200, 33], [600, 201], False, 0),
+    (4, 2, 64, 256, [100, 9], [129, 250], True, 0),            # 127 and 6 NaN slots in the last 128-row box
+    (6, 2, 128, 16, [30, 3], [0, 140], True, 0),               # an empty cache
+    (12, 4, 64, 16, [1, 1, 1, 1], [1, 128, 129, 515], True, 0),
+    (16, 1, 128, 32, [40], [127], True, 33),
+]
+
+
+def gathered(p, lens):
+    """The caches of all sequences, packed one after another, in float64."""
+    ks, vs = [], []
+    for b, L in enumerate(lens):
+        for pool, to in ((p.k_pool, ks), (p.v_pool, vs)):
+            to.append(sdpa.gather_pages(pool, p.page_table[b].numpy(), L, p.page_size))
+    return np.concatenate(ks), np.concatenate(vs)
+
+
+@pytest.mark.parametrize("case", PAGED, ids=[str(c) for c in PAGED])
+def test_packed_chunks_over_the_paged_cache(case):
+    Hq, Hkv, D, page, new, lens, causal, window = case
+    p = inputs.paged_inputs(len(lens), Hq, Hkv, D, page, seed=sum(lens) + D, seq_lens=lens, spare_pages=3, poison=True)
+    q = inputs.normal((sum(new) + 5, Hq, D), 77)
+    q[sum(new):] = float("nan")
+    cu = cumulative(new)
+    api.attn_device_status(clear=True)
+    got = api.attn_prefill_packed_paged(q.cuda(), p.k_pool.cuda(), p.v_pool.cuda(), cu.cuda(), p.page_table.cuda(),
+                                        p.seq_lens.cuda(), max_seq_len=max(lens), causal=causal, window=window,
+                                        want_lse=True)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 0
+    K, V = gathered(p, lens)
+    assert_packed(got, packed_attention(f64(q), K, V, cu.tolist(), cumulative(lens).tolist(), D ** -0.5, causal,
+                                        window), str(case))
+
+
+def test_paged_and_dense_packed_agree_to_the_bit():
+    Hq, Hkv, D, page, lens = 8, 2, 128, 16, [300, 17, 129]
+    p = inputs.paged_inputs(3, Hq, Hkv, D, page, seed=3, seq_lens=lens)
+    q = inputs.normal((sum(lens), Hq, D), 5).cuda()
+    K, V = (torch.from_numpy(x).to(torch.bfloat16).cuda() for x in gathered(p, lens))
+    cu = cumulative(lens).cuda()
+    dense = api.attn_prefill_packed(q, K, V, cu, window=100)
+    paged = api.attn_prefill_packed_paged(q, p.k_pool.cuda(), p.v_pool.cuda(), cu, p.page_table.cuda(),
+                                          p.seq_lens.cuda(), max_seq_len=300, window=100)
+    torch.cuda.synchronize()
+    assert torch.equal(dense, paged)
+
+
+def test_an_empty_cache_of_no_pages():
+    q = inputs.normal((9, 4, 64), 1).cuda()
+    pool = torch.empty((0, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = api.attn_prefill_packed_paged(q, pool, pool, cumulative([4, 5]).cuda(),
+                                             torch.empty((2, 0), dtype=torch.int32, device="cuda"),
+                                             torch.zeros(2, dtype=torch.int32, device="cuda"), max_seq_len=0,
+                                             want_lse=True)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 0
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_a_bad_page_is_reported_and_not_read():
+    lens, new = [100, 60], [30, 20]
+    p = inputs.paged_inputs(2, 4, 2, 64, 16, seed=2, seq_lens=lens)
+    table = p.page_table.clone()
+    table[0, 3] = p.num_pages + 77
+    table[0, 5] = -4
+    q = inputs.normal((50, 4, 64), 3)
+    cu = cumulative(new)
+    api.attn_device_status(clear=True)
+    out, lse = api.attn_prefill_packed_paged(q.cuda(), p.k_pool.cuda(), p.v_pool.cuda(), cu.cuda(), table.cuda(),
+                                             p.seq_lens.cuda(), max_seq_len=100, want_lse=True)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 5
+    K, V = gathered(p, lens)
+    want = packed_attention(f64(q), K, V, cu.tolist(), cumulative(lens).tolist(), 1 / 8)
+    ok = [w[30:] for w in want]
+    assert_packed((out[30:], lse[30:]), ok, "the other sequence")
+
+
+@pytest.mark.parametrize("cu", [[0, 60, 40, 100], [0, 30, 60, 400], [-20, 10, 60, 100], [0, 2 ** 31 - 1, 5, -2 ** 31]])
+def test_malformed_cumulative_lengths_are_reported_and_stay_in_the_buffers(cu):
+    q, k, v = (x.cuda() for x in tensors(100, 100, 4, 2, 64, 3))
+    guard = torch.full((300, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = guard[100:200]
+    api.attn_device_status(clear=True)
+    api.attn_prefill_packed(q, k, v, torch.tensor(cu, dtype=torch.int32, device="cuda"), out=out)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 5
+    assert (guard[:100] == 9).all() and (guard[200:] == 9).all()
+    # the library goes on as before
+    good = cumulative([40, 60])
+    got = run_packed(q.cpu(), k.cpu(), v.cpu(), good)
+    assert_packed(got, packed_attention(f64(q), f64(k), f64(v), good.tolist(), good.tolist(), 1 / 8))
+
+
+def test_a_sequence_longer_than_max_seq_len_is_cut_and_reported():
+    p = inputs.paged_inputs(1, 4, 2, 64, 16, seed=2, seq_lens=[100])
+    q = inputs.normal((10, 4, 64), 3).cuda()
+    api.attn_device_status(clear=True)
+    out = api.attn_prefill_packed_paged(q, p.k_pool.cuda(), p.v_pool.cuda(), cumulative([10]).cuda(),
+                                        p.page_table.cuda(), p.seq_lens.cuda(), max_seq_len=64)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 5
+    assert torch.isfinite(out.float()).all()
+
+
+def test_a_captured_graph_is_replayed_with_other_lengths_while_another_runs():
+    Hq, Hkv, D, T = 8, 2, 128, 600
+    q, k, v = (x.cuda() for x in tensors(T, T, Hq, Hkv, D, 50))
+    streams, graphs, cus, outs = [], [], [], []
+    for i in range(2):
+        cu = cumulative([100, 100, 100, 100, 100]).cuda()
+        out = torch.zeros_like(q)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            api.attn_prefill_packed(q, k, v, cu, out=out)
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            api.attn_prefill_packed(q, k, v, cu, out=out)
+        streams.append(s), graphs.append(g), cus.append(cu), outs.append(out)
+    for lens in ([600, 0, 0, 0, 0], [1, 2, 3, 4, 5], [0, 0, 0, 0, 0], [120, 120, 120, 120, 120]):
+        other = [x // 2 for x in lens]
+        for cu, n, out in zip(cus, (lens, other), outs):
+            cu.copy_(cumulative(n))
+            out.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):       # both in flight at once
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert api.attn_device_status(clear=True) == 0
+        for n, out in ((lens, outs[0]), (other, outs[1])):
+            eager = torch.zeros_like(q)
+            api.attn_prefill_packed(q, k, v, cumulative(n).cuda(), out=eager)
+            torch.cuda.synchronize()
+            assert torch.equal(eager, out)
+    del graphs
+
+
+def test_a_call_on_another_stream_with_its_own_result():
+    q, k, v = (x.cuda() for x in tensors(500, 500, 8, 2, 64, 60))
+    cu = cumulative([300, 200]).cuda()
+    want = api.attn_prefill_packed(q, k, v, cu)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    out = api.attn_prefill_packed(q, k, v, cu, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want)

@@ -1,0 +1,164 @@
+"""Host-side checks of the packed operators: what the C ABI and the binding refuse before any launch.  CPU only."""
+import ctypes
+
+import pytest
+import torch
+
+from scaled_dot_product_prefill_b200 import _lib, api
+
+FAKE = ctypes.c_void_p(0x10000)          # aligned, never dereferenced: every case fails validation or is empty
+OFF8 = ctypes.c_void_p(0x10008)
+OFF2 = ctypes.c_void_p(0x10002)
+bf = torch.bfloat16
+
+
+def lib():
+    return _lib.load()
+
+
+def packed(q=FAKE, k=FAKE, v=FAKE, cu_q=FAKE, cu_k=FAKE, B=2, Tq=64, Tk=64, Hq=8, Hkv=2, D=64, qs=512, ks=128, vs=128,
+           os=512, scale=0.125, causal=1, window=0, out=FAKE, lse=None):
+    return lib().attn_prefill_packed(q, k, v, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, qs, ks, vs, os, scale, causal, window,
+                                     out, lse, None)
+
+
+def paged(q=FAKE, kp=FAKE, vp=FAKE, cu_q=FAKE, pt=FAKE, sl=FAKE, page=16, B=2, Tq=64, Hq=8, Hkv=2, D=64, qs=512, os=512,
+          num_pages=8, max_pages=4, max_seq_len=64, scale=0.125, causal=1, window=0, out=FAKE, lse=None):
+    return lib().attn_prefill_packed_paged(q, kp, vp, cu_q, pt, sl, page, B, Tq, Hq, Hkv, D, qs, os, num_pages, max_pages,
+                                           max_seq_len, scale, causal, window, out, lse, None)
+
+
+BOTH = [
+    (dict(q=None), 1), (dict(out=None), 1), (dict(cu_q=None), 1), (dict(q=OFF8), 1), (dict(out=OFF8), 1),
+    (dict(cu_q=OFF2), 1), (dict(lse=OFF2), 1), (dict(Hq=6, Hkv=4, qs=384, os=384), 1), (dict(Hkv=0), 1),
+    (dict(Tq=-1), 1), (dict(B=-1), 1), (dict(scale=0.0), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1), (dict(causal=2), 1), (dict(window=-1), 1), (dict(D=96, qs=768, os=768), 1),
+    (dict(D=256, qs=2048, os=2048), 1),
+    (dict(qs=504), 1), (dict(qs=516), 1), (dict(os=0), 1), (dict(qs=-512), 1), (dict(os=1 << 40), 1),
+    (dict(causal=0, window=4), 2), (dict(B=70000), 2), (dict(Tq=(1 << 30) + 1), 2),
+    (dict(B=0, q=None, out=None, cu_q=None), 0), (dict(Tq=0, q=None, out=None), 0), (dict(Hq=0, q=None, out=None), 0),
+]
+
+
+@pytest.mark.parametrize("change,status", BOTH, ids=[str(c) for c, _ in BOTH])
+def test_both_packed_prefills_refuse(change, status):
+    assert packed(**change) == status
+    assert paged(**change) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(cu_k=None), 1), (dict(k=OFF8), 1), (dict(cu_k=OFF2), 1),
+    (dict(Tk=-1), 1), (dict(ks=120), 1), (dict(vs=132), 1), (dict(Tk=(1 << 30) + 1), 2), (dict(B=0, Tk=-1), 1)])
+def test_packed_prefill_refuses(change, status):
+    assert packed(**change) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(kp=None), 1), (dict(vp=None), 1), (dict(pt=None), 1), (dict(sl=None), 1), (dict(kp=OFF8), 1),
+    (dict(pt=OFF2), 1), (dict(sl=OFF2), 1), (dict(num_pages=0), 1), (dict(max_pages=0), 1), (dict(num_pages=-1), 1),
+    (dict(max_seq_len=-1), 1), (dict(page=0), 1), (dict(page=8), 2), (dict(page=48), 2), (dict(page=512), 2),
+    (dict(num_pages=0x7FFFFFFF), 2), (dict(max_seq_len=(1 << 30) + 1), 2)])
+def test_packed_paged_prefill_refuses(change, status):
+    assert paged(**change) == status
+
+
+def append(fp8=False, q=FAKE, k=FAKE, v=FAKE, qo=FAKE, ko=None, kp=FAKE, vp=FAKE, table=FAKE, cu=FAKE, pt=FAKE, sl=FAKE,
+           page=16, B=2, T=6, Hq=8, Hkv=2, D=64, rot=64, inter=0, qs=512, ks=128, vs=128, qos=512, kos=128, num_pages=8,
+           max_pages=4, max_pos=64, scales=(1.0, 1.0)):
+    args = [q, k, v, qo, ko, kp, vp, table, cu, pt, sl, page, B, T, Hq, Hkv, D, rot, inter, qs, ks, vs, qos, kos,
+            num_pages, max_pages, max_pos]
+    if fp8:
+        return lib().attn_kv_append_rope_fp8(*args, *scales, None)
+    return lib().attn_kv_append_rope(*args, None)
+
+
+APPEND = [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(q=None), 1), (dict(qo=None), 1), (dict(kp=None), 1), (dict(vp=None), 1),
+    (dict(table=None), 1), (dict(pt=None), 1), (dict(sl=None), 1), (dict(q=OFF8), 1), (dict(ko=OFF8), 1),
+    (dict(table=OFF8), 1), (dict(cu=OFF2), 1), (dict(pt=OFF2), 1), (dict(B=-1), 1), (dict(T=-1), 1), (dict(Hq=-1), 1),
+    (dict(rot=-16), 1), (dict(rot=80), 1), (dict(inter=2), 1), (dict(page=0), 1), (dict(num_pages=0), 1),
+    (dict(max_pages=0), 1), (dict(max_pos=0), 1), (dict(max_pos=-1), 1), (dict(cu=None, T=7), 1),
+    (dict(qs=500), 1), (dict(ks=64), 1), (dict(vs=129), 1), (dict(qos=0), 1), (dict(ko=FAKE, k=ctypes.c_void_p(0x20000), kos=0), 1),
+    (dict(q=FAKE, qo=FAKE, qos=1024), 1), (dict(ko=FAKE, k=FAKE, kos=256), 1),
+    (dict(D=72, rot=64, qs=576, qos=576, ks=144, vs=144), 2), (dict(D=528, qs=4224, qos=4224, ks=1056, vs=1056), 2),
+    (dict(rot=24), 2), (dict(page=12), 2),
+    (dict(B=0, k=None), 0), (dict(T=0, k=None), 0), (dict(Hkv=0, k=None), 0),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("change,status", APPEND, ids=[str(c) for c, _ in APPEND])
+def test_rotating_append_refuses(change, status, fp8):
+    assert append(fp8, **change) == status
+
+
+@pytest.mark.parametrize("scales", [(0.0, 1.0), (1.0, -1.0), (float("nan"), 1.0), (1.0, float("inf"))])
+def test_rotating_append_refuses_bad_scales(scales):
+    assert append(True, scales=scales) == 1
+
+
+def t(*shape, dtype=bf):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def i32(*shape):
+    return t(*shape, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("match,args,kw", [
+    ("bfloat16", (t(6, 8, 64).float(), t(6, 2, 64), t(6, 2, 64), i32(3)), {}),
+    (r"must be \[tokens", (t(6, 8 * 64), t(6, 2, 64), t(6, 2, 64), i32(3)), {}),
+    ("k must have shape", (t(6, 8, 64), t(6, 2, 128), t(6, 2, 64), i32(3)), {}),
+    ("v must have shape", (t(6, 8, 64), t(6, 2, 64), t(5, 2, 64), i32(3)), {}),
+    ("without cu_seqlens_k", (t(6, 8, 64), t(7, 2, 64), t(7, 2, 64), i32(3)), {}),
+    ("cu_seqlens_q must have shape", (t(6, 8, 64), t(6, 2, 64), t(6, 2, 64), i32(3, 1)), {}),
+    ("cu_seqlens_q must be", (t(6, 8, 64), t(6, 2, 64), t(6, 2, 64), t(3, dtype=torch.int64)), {}),
+    ("cu_seqlens_k must be", (t(6, 8, 64), t(6, 2, 64), t(6, 2, 64), i32(3), i32(4)), {}),
+    ("cu_seqlens_q must be", (t(6, 8, 64), t(6, 2, 64), t(6, 2, 64), i32(6)[::2]), {}),
+    ("out must have shape", (t(6, 8, 64), t(6, 2, 64), t(6, 2, 64), i32(3)), dict(out=t(6, 8, 128))),
+    ("out must be a bfloat16", (t(6, 8, 64), t(6, 2, 64), t(6, 2, 64), i32(3)), dict(out=t(6, 8, 64).float())),
+    ("lse must be", (t(6, 8, 64), t(6, 2, 64), t(6, 2, 64), i32(3)), dict(lse=t(8, 6, dtype=torch.float32))),
+    ("heads contiguous", (t(8, 6, 64).transpose(0, 1), t(6, 2, 64), t(6, 2, 64), i32(3)), {}),
+    ("heads contiguous", (t(6, 8, 128)[..., ::2], t(6, 2, 64), t(6, 2, 64), i32(3)), {}),
+    ("heads contiguous", (t(6, 8, 64), t(1, 2, 64).expand(6, 2, 64), t(6, 2, 64), i32(3)), {}),
+    ("heads contiguous", (t(6, 8, 64), t(6, 2, 64), t(6, 2 * 64 + 4)[:, :128].view(6, 2, 64), i32(3)), {}),
+    ("CUDA", (t(6, 8, 64), t(6, 2, 64), t(6, 2, 64), i32(3)), {}),
+])
+def test_the_binding_refuses_packed_tensors(match, args, kw):
+    with pytest.raises(ValueError, match=match):
+        api.attn_prefill_packed(*args, **kw)
+
+
+def test_the_binding_refuses_packed_paged_tensors():
+    q, pool, cu, pt, sl = t(6, 8, 64), t(4, 2, 16, 64), i32(3), i32(2, 3), i32(2)
+    call = lambda *a: api.attn_prefill_packed_paged(*a, max_seq_len=32)  # noqa: E731
+    for match, args in [
+            ("page_table must be", (q, pool, pool, cu, i32(1, 3), sl)), ("seq_lens must be", (q, pool, pool, cu, pt, i32(3))),
+            ("page_table must be", (q, pool, pool, cu, pt.long(), sl)), ("v_pool must be", (q, pool, t(4, 2, 16, 128), cu, pt, sl)),
+            ("k_pool must be", (q, t(4, 2, 16, 128), pool, cu, pt, sl)), ("k_pool must be", (q, pool.float(), pool, cu, pt, sl)),
+            ("the pools", (q, pool[0], pool, cu, pt, sl)), ("CUDA", (q, pool, pool, cu, pt, sl))]:
+        with pytest.raises(ValueError, match=match):
+            call(*args)
+
+
+def test_the_binding_refuses_append_tensors():
+    q, k, pool, tab, pt, sl = t(6, 8, 64), t(6, 2, 64), t(4, 2, 16, 64), t(9, 64, dtype=torch.float32), i32(2, 3), i32(2)
+    for match, args, kw in [
+            ("v must have shape", (q, k, t(5, 2, 64), pool, pool, tab, pt, sl), {}),
+            ("q must have shape", (t(5, 8, 64), k, k, pool, pool, tab, pt, sl), {}),
+            ("q_out must have shape", (q, k, k, pool, pool, tab, pt, sl), dict(q_out=t(6, 4, 64))),
+            ("q_out needs q", (None, k, k, pool, pool, tab, pt, sl), dict(q_out=q)),
+            ("k_out must have shape", (q, k, k, pool, pool, tab, pt, sl), dict(k_out=q)),
+            ("cos_sin must be", (q, k, k, pool, pool, tab.double(), pt, sl), {}),
+            ("cos_sin must be", (q, k, k, pool, pool, tab.t(), pt, sl), {}),
+            ("at most 64 columns", (q, k, k, pool, pool, t(9, 128, dtype=torch.float32), pt, sl), {}),
+            ("k_pool must be", (q, k, k, pool.view(torch.uint8), pool, tab, pt, sl), {}),
+            ("v_pool must be", (q, k, k, pool, t(4, 2, 8, 64), tab, pt, sl), {}),
+            ("seq_lens must be", (q, k, k, pool, pool, tab, pt, i32(3)), {}),
+            ("cu_seqlens must be", (q, k, k, pool, pool, tab, pt, sl), dict(cu_seqlens=i32(4))),
+            ("same number of each", (q, k, k, pool, pool, tab, i32(4, 3), i32(4)), {}),
+            ("CUDA", (q, k, k, pool, pool, tab, pt, sl), {})]:
+        with pytest.raises(ValueError, match=match):
+            api.attn_kv_append_rope(*args, **kw)
+    with pytest.raises(ValueError, match="k_pool must be"):
+        api.attn_kv_append_rope_fp8(q, k, k, pool, pool, tab, pt, sl, k_scale=1, v_scale=1)
