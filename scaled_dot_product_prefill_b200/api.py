@@ -458,65 +458,73 @@ def attn_kv_append_fp8(k_new, v_new, k_pool, v_pool, page_table, seq_lens, *, k_
         S_new, D, num_pages, page_table.shape[1], float(k_scale), float(v_scale), _stream(stream)))
 
 
-def _packed(t, name, heads, D, like=None):
+# The packed calls run at latencies of a few microseconds, so their checks cost as few Python
+# steps as they can: one comparison per tensor for shape, type, strides and device.
+
+def _packed(t, name, T, heads, D):
     """Token stride of a packed [T, heads, D] bf16 tensor (any stride between tokens, heads side by side)."""
-    if t.dim() != 3 or t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be a bfloat16 [tokens, heads, D] tensor, got {t.dtype} {tuple(t.shape)}")
-    T, H, d = t.shape
-    if H != heads or d != D or (like is not None and T != like):
-        raise ValueError(f"{name} must have shape {(T if like is None else like, heads, D)}, got {tuple(t.shape)}")
+    if t.shape != (T, heads, D):
+        raise ValueError(f"{name} must have shape {(T, heads, D)}, got {tuple(t.shape)}")
     s0, s1, s2 = t.stride()
     row = heads * D
-    if T <= 1:
-        s0 = row if s0 < row or s0 % 8 else s0
-    if T and row and ((s2 != 1 and D > 1) or (s1 != D and heads > 1) or s0 < row or s0 % 8):
+    if s2 == 1 and s1 == D and s0 >= row and s0 % 8 == 0:
+        return s0
+    # a dimension of one element has any stride, an empty tensor any
+    if T <= 1 or row == 0:
+        s0 = row
+    if row and T and ((s2 != 1 and D > 1) or (s1 != D and heads > 1) or s0 < row or s0 % 8):
         raise ValueError(f"{name} must have its heads contiguous and a token stride that is a multiple of 8 and at "
-                         f"least {row}, got strides {(s0, s1, s2)}")
-    return s0 if row else 0
+                         f"least {row}, got strides {(t.stride())}")
+    return s0
 
 
-def _on_device(*named):
-    """Every (tensor, name) lies on the current CUDA device; contiguity is the caller's matter."""
-    dev = None
-    for t, name in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor on the current device")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
-
-
-def _int32(t, name, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _contiguous(t, name, shape, dtype):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+def _shaped(t, name, shape, dtype):
+    """Data pointer of a contiguous tensor of this shape and type."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _made_here(stream, *ts):
-    """Tensors allocated on the current stream for a call on another one: kept from early reuse."""
-    if stream is not None and stream != torch.cuda.current_stream():
-        for t in ts:
-            if t is not None:
-                t.record_stream(stream)
+def _on_device(tensors, names):
+    """The device index of every tensor that is not None: the current CUDA device."""
+    dev = tensors[0].get_device()
+    for t, name in zip(tensors, names):
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _cuda_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _raw_stream(stream, dev, *made):
+    """The stream handle; tensors made here on the current stream for a call on another are kept from early reuse."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if made and stream != torch.cuda.current_stream():
+        for t in made:
+            t.record_stream(stream)
+    return stream.cuda_stream
 
 
 def _batch_of(cu, name):
     if cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError(f"{name} must have shape [B + 1], got {tuple(cu.shape)}")
     return cu.shape[0] - 1
+
+
+def _packed_results(q, Tq, Hq, D, out, lse, want_lse):
+    """out, its token stride, lse, its pointer, and what was allocated for them here."""
+    made = ()
+    if out is None:
+        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
+        made = (out,)
+    if lse is None and want_lse:
+        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+        made += (lse,)
+    return (out, _packed(out, "out", Tq, Hq, D), lse,
+            None if lse is None else _shaped(lse, "lse", (Tq, Hq), torch.float32), made)
 
 
 def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True, window=0, scale=None, out=None,
@@ -533,32 +541,23 @@ def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True
         raise ValueError("q, k and v must be [tokens, heads, D]")
     Tq, Hq, D = q.shape
     Tk, Hkv, _ = k.shape
-    q_stride = _packed(q, "q", Hq, D)
-    k_stride = _packed(k, "k", Hkv, D)
-    v_stride = _packed(v, "v", Hkv, D, like=Tk)
+    q_stride = _packed(q, "q", Tq, Hq, D)
+    k_stride = _packed(k, "k", Tk, Hkv, D)
+    v_stride = _packed(v, "v", Tk, Hkv, D)
     B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
     if cu_seqlens_k is None:
         if Tk != Tq:
             raise ValueError(f"without cu_seqlens_k, k and v must have q's {Tq} rows, got {Tk}")
         cu_seqlens_k = cu_seqlens_q
-    cu_q = _int32(cu_seqlens_q, "cu_seqlens_q", (B + 1,))
-    cu_k = _int32(cu_seqlens_k, "cu_seqlens_k", (B + 1,))
-    made = []
-    if out is None:
-        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
-        made.append(out)
-    if lse is None and want_lse:
-        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
-        made.append(lse)
-    out_stride = _packed(out, "out", Hq, D, like=Tq)
-    lse_ptr = None if lse is None else _contiguous(lse, "lse", (Tq, Hq), torch.float32)
-    _on_device((q, "q"), (k, "k"), (v, "v"), (cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k"),
-               (out, "out"), (lse, "lse"))
-    _made_here(stream, *made)
+    cu_q = _shaped(cu_seqlens_q, "cu_seqlens_q", (B + 1,), torch.int32)
+    cu_k = _shaped(cu_seqlens_k, "cu_seqlens_k", (B + 1,), torch.int32)
+    out, out_stride, lse, lse_ptr, made = _packed_results(q, Tq, Hq, D, out, lse, want_lse)
+    dev = _on_device((q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse),
+                     ("q", "k", "v", "cu_seqlens_q", "cu_seqlens_k", "out", "lse"))
     _check("attn_prefill_packed", _lib.load().attn_prefill_packed(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
         out_stride, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)), int(window),
-        out.data_ptr(), lse_ptr, _cuda_stream(stream)))
+        out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
     return out if lse is None else (out, lse)
 
 
@@ -574,31 +573,22 @@ def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_l
         raise ValueError("q must be [tokens,Hq,D], the pools [num_pages,Hkv,page_size,D], page_table [B,max_pages]")
     Tq, Hq, D = q.shape
     num_pages, Hkv, page_size, _ = k_pool.shape
-    q_stride = _packed(q, "q", Hq, D)
+    q_stride = _packed(q, "q", Tq, Hq, D)
     B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
     max_pages = page_table.shape[1]
     pool = (num_pages, Hkv, page_size, D)
-    kp = _contiguous(k_pool, "k_pool", pool, torch.bfloat16)
-    vp = _contiguous(v_pool, "v_pool", pool, torch.bfloat16)
-    cu_q = _int32(cu_seqlens_q, "cu_seqlens_q", (B + 1,))
-    table = _int32(page_table, "page_table", (B, max_pages))
-    lens = _int32(seq_lens, "seq_lens", (B,))
-    made = []
-    if out is None:
-        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
-        made.append(out)
-    if lse is None and want_lse:
-        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
-        made.append(lse)
-    out_stride = _packed(out, "out", Hq, D, like=Tq)
-    lse_ptr = None if lse is None else _contiguous(lse, "lse", (Tq, Hq), torch.float32)
-    _on_device((q, "q"), (k_pool, "k_pool"), (v_pool, "v_pool"), (cu_seqlens_q, "cu_seqlens_q"),
-               (page_table, "page_table"), (seq_lens, "seq_lens"), (out, "out"), (lse, "lse"))
-    _made_here(stream, *made)
+    kp = _shaped(k_pool, "k_pool", pool, torch.bfloat16)
+    vp = _shaped(v_pool, "v_pool", pool, torch.bfloat16)
+    cu_q = _shaped(cu_seqlens_q, "cu_seqlens_q", (B + 1,), torch.int32)
+    table = _shaped(page_table, "page_table", (B, max_pages), torch.int32)
+    lens = _shaped(seq_lens, "seq_lens", (B,), torch.int32)
+    out, out_stride, lse, lse_ptr, made = _packed_results(q, Tq, Hq, D, out, lse, want_lse)
+    dev = _on_device((q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, out, lse),
+                     ("q", "k_pool", "v_pool", "cu_seqlens_q", "page_table", "seq_lens", "out", "lse"))
     _check("attn_prefill_packed_paged", _lib.load().attn_prefill_packed_paged(
         q.data_ptr(), kp, vp, cu_q, table, lens, page_size, B, Tq, Hq, Hkv, D, q_stride, out_stride, num_pages,
         max_pages, int(max_seq_len), 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)),
-        int(window), out.data_ptr(), lse_ptr, _cuda_stream(stream)))
+        int(window), out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
     return out if lse is None else (out, lse)
 
 
@@ -610,47 +600,46 @@ def _append_rope(name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table,
     T, Hkv, D = k.shape
     num_pages, _, page_size, _ = k_pool.shape
     B, max_pages = page_table.shape
-    k_stride, v_stride = _packed(k, "k", Hkv, D), _packed(v, "v", Hkv, D, like=T)
-    Hq = q_stride = q_out_stride = k_out_stride = 0
-    made = []
+    k_stride, v_stride = _packed(k, "k", T, Hkv, D), _packed(v, "v", T, Hkv, D)
+    Hq = q_stride = q_out_stride = k_out_stride = max_pos = rot = 0
+    q_ptr = q_out_ptr = k_out_ptr = angles = cu = None
+    made = ()
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [tokens, Hq, D]")
         Hq = q.shape[1]
-        q_stride = _packed(q, "q", Hq, D, like=T)
+        q_stride = _packed(q, "q", T, Hq, D)
         if q_out is None:
             q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-            made.append(q_out)
-        q_out_stride = _packed(q_out, "q_out", Hq, D, like=T)
+            made = (q_out,)
+        q_out_stride = _packed(q_out, "q_out", T, Hq, D)
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if k_out is not None:
-        k_out_stride = _packed(k_out, "k_out", Hkv, D, like=T)
+        k_out_stride = _packed(k_out, "k_out", T, Hkv, D)
+        k_out_ptr = k_out.data_ptr()
     pool = (num_pages, Hkv, page_size, D)
-    kp, vp = _contiguous(k_pool, "k_pool", pool, pool_dtype), _contiguous(v_pool, "v_pool", pool, pool_dtype)
-    max_pos = rot = 0
+    kp, vp = _shaped(k_pool, "k_pool", pool, pool_dtype), _shaped(v_pool, "v_pool", pool, pool_dtype)
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous float32 [max_pos, rot_dim] tensor")
+        if cos_sin.dim() != 2 or cos_sin.shape[1] > D:
+            raise ValueError(f"cos_sin must have shape [max_pos, rot_dim] with at most {D} columns, got "
+                             f"{tuple(cos_sin.shape)}")
         max_pos, rot = cos_sin.shape
-        if rot > D:
-            raise ValueError(f"cos_sin must have at most {D} columns, got {rot}")
-    table = _int32(page_table, "page_table", (B, max_pages))
-    lens = _int32(seq_lens, "seq_lens", (B,))
-    cu = None
+        angles = _shaped(cos_sin, "cos_sin", (max_pos, rot), torch.float32)
+    table = _shaped(page_table, "page_table", (B, max_pages), torch.int32)
+    lens = _shaped(seq_lens, "seq_lens", (B,), torch.int32)
     if cu_seqlens is not None:
-        cu = _int32(cu_seqlens, "cu_seqlens", (B + 1,))
+        cu = _shaped(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32)
     elif B and T % B:
         raise ValueError(f"without cu_seqlens the {T} tokens must be the same number of each of {B} sequences")
-    _on_device((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"), (k_out, "k_out"), (k_pool, "k_pool"),
-               (v_pool, "v_pool"), (cos_sin, "cos_sin"), (page_table, "page_table"), (seq_lens, "seq_lens"),
-               (cu_seqlens, "cu_seqlens"))
-    _made_here(stream, *made)
+    dev = _on_device((k, v, q, q_out, k_out, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens),
+                     ("k", "v", "q", "q_out", "k_out", "k_pool", "v_pool", "cos_sin", "page_table", "seq_lens",
+                      "cu_seqlens"))
     _check(name, getattr(_lib.load(), name)(
-        None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), None if q is None else q_out.data_ptr(),
-        None if k_out is None else k_out.data_ptr(), kp, vp, None if cos_sin is None else cos_sin.data_ptr(), cu, table,
-        lens, page_size, B, T, Hq, Hkv, D, rot, int(bool(interleaved)), q_stride, k_stride, v_stride, q_out_stride,
-        k_out_stride, num_pages, max_pages, max_pos, *scales, _cuda_stream(stream)))
+        q_ptr, k.data_ptr(), v.data_ptr(), q_out_ptr, k_out_ptr, kp, vp, angles, cu, table, lens, page_size, B, T, Hq,
+        Hkv, D, rot, 1 if interleaved else 0, q_stride, k_stride, v_stride, q_out_stride, k_out_stride, num_pages,
+        max_pages, max_pos, *scales, _raw_stream(stream, dev, *made)))
     return q_out
 
 

@@ -19,8 +19,7 @@
 //              of shared-memory slots (128-byte swizzle, no multicast); one
 //              thread for dense K/V, the whole warp for page boxes
 //   warp 9     MMA issuer (one thread) and tensor-memory owner
-//   warps 10-11 idle (complete the third warpgroup for the register split);
-//              PACKED: item scheduler, and zeroing of V rows behind a sequence
+//   warps 10-11 idle (complete the third warpgroup for the register split)
 // Tensor memory (512 columns x 128 lanes, fp32):
 //   S_i = Q_i K_j^T   columns [128 i, 128 i + 128)      (A and B in smem)
 //   P_i (bf16)        written over the first 64 columns of S_i by the softmax
@@ -41,23 +40,6 @@
 // computes S_i(j+1) while the exponentials of tile j run, and each P_i V_j
 // signals its own completion.  PAGED kernels read K/V through a page table
 // as page-sized TMA boxes.
-//
-// PACKED kernels (attn_prefill_packed, attn_prefill_packed_paged) take
-// sequences of different lengths, one after another in [tokens, heads, D]
-// buffers.  Three things differ from the dense kernel:
-// * A query tile is 128 / 2^s tokens x 2^s query heads of one kv head (2^s:
-//   the largest power of two that divides the group), one four-dimensional
-//   TMA box.  A sequence of n tokens then fills n * 2^s rows of its last
-//   tile instead of n, and each K/V tile serves 2^s heads at once.
-// * The lengths are on the device, so warp 10 makes the items: it walks the
-//   blocks of all sequences from the costliest (last visible key farthest)
-//   down, deals them out in the dense kernel's snake, and hands each to the
-//   other roles through a ring in shared memory.  Nothing is stored and
-//   no other launch precedes this one.
-// * The last key tile of a sequence is followed in memory by the next
-//   sequence's rows.  Their scores are masked like any others; the V rows
-//   are zeroed in shared memory (0 * NaN is NaN) by warp 11 while the softmax
-//   of that tile runs.
 #include <cmath>
 #include <cstdint>
 #include <cuda.h>
@@ -74,8 +56,6 @@ constexpr int BM = 128;          // query rows per tile
 constexpr int NQ = 2;            // query tiles per work item
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kSchedWarp = 10;   // PACKED
-constexpr int kTailWarp = 11;    // PACKED
 constexpr float kTau = 8.0f;     // lazy-rescale threshold, log2 units
 
 template <int D>
@@ -110,10 +90,6 @@ struct Cfg {
   static constexpr size_t SMEM = 1024 /*align*/ + QBUF * NQ * Q_BYTES + STAGES * TILE_BYTES + 256;
 };
 
-constexpr int kItemRing = 4;           // PACKED: items handed out ahead
-constexpr int kItemConsumers = 11;     // TMA warp, MMA thread, V-zeroing warp, 8 softmax warps
-constexpr size_t kPackedSmem = 512;    // shared memory of the item ring and its barriers
-
 struct Params {
   int B, Hq, Hkv, Sq, Skv, causal, window, n_qblocks, n_items;
   float scale_log2;
@@ -126,24 +102,12 @@ struct Params {
   const int32_t* page_table;
   const int32_t* seq_lens;
   int page_size, box_rows, max_pages, num_pages;
-  // packed sequences (the PACKED kernels): sequence b owns rows [cu_q[b], cu_q[b + 1])
-  // of q and out, and rows [cu_k[b], cu_k[b + 1]) of k and v (unless PAGED)
-  const int32_t* cu_q;
-  const int32_t* cu_k;
-  int Tq, Tk;               // rows of q and out, of k and v
-  int pack_log2;            // s: 2^s query heads of a kv head share a tile
-  int head_blocks;          // Hq >> s
-  int tiles;                // query tiles per item, 1 or 2
-  long long out_stride;     // elements from one token of out to the next
 };
 
 struct Item {
   int bh, b, g, q_row0, skv;   // skv: keys of this item's sequence
   int lo[NQ], hi[NQ];   // key-tile range per query tile (empty if hi <= lo)
   int lo_all, hi_all;   // union; empty if hi_all <= lo_all
-  // PACKED: bh is the head block, b < 0 ends the list, q_row0 and q_end are tokens of
-  // the sequence (its block is [q_row0, q_end)), q_base and k_base its first rows
-  int q_base, k_base, sq, q_end;
 };
 
 // The r-th item of this CTA (snake over cost-ordered items), or -1.
@@ -201,111 +165,6 @@ __device__ __forceinline__ Item make_item(const Params& p, int k) {
   return it;
 }
 
-// One sequence of a packed batch: first rows and lengths, cut to the buffers.
-// A cumulative length that decreases or passes the buffer is reported, and
-// never leads outside it.
-struct PackedSpan {
-  int q0, sq, k0, sk;
-};
-
-template <bool PAGED>
-__device__ __forceinline__ PackedSpan packed_span(const Params& p, int b) {
-  PackedSpan s;
-  const int a = p.cu_q[b], e = p.cu_q[b + 1];
-  bool bad = a < 0 || e < a || e > p.Tq;
-  s.q0 = min(max(a, 0), p.Tq);
-  s.sq = min(max(e, s.q0), p.Tq) - s.q0;
-  if constexpr (PAGED) {
-    const int L = p.seq_lens[b];
-    const long long room = static_cast<long long>(p.max_pages) * p.page_size;
-    const int cap = room < p.Skv ? static_cast<int>(room) : p.Skv;
-    bad |= L > cap;
-    s.k0 = 0;
-    s.sk = max(0, min(L, cap));
-  } else {
-    const int ka = p.cu_k[b], ke = p.cu_k[b + 1];
-    bad |= ka < 0 || ke < ka || ke > p.Tk;
-    s.k0 = min(max(ka, 0), p.Tk);
-    s.sk = min(max(ke, s.k0), p.Tk) - s.k0;
-  }
-  if (bad) record_error(p.err, ATTN_ERRBIT_BADPAGE);
-  return s;
-}
-
-// How a sequence's query blocks (of 2^tb_log2 tokens) spread over cost levels.
-// Causal: block qb ends level qb + o, o = ceil((sk - sq) / block), whose last
-// visible key lies in key block level - 1; blocks that see no key or only
-// the first block's share level 0.  Not causal: all blocks cost the same, one
-// level by the number of keys.
-struct PackedLevels {
-  int o, nb;
-};
-
-template <bool PAGED>
-__device__ __forceinline__ PackedLevels packed_levels(const Params& p, int b, int tb_log2) {
-  const PackedSpan s = packed_span<PAGED>(p, b);
-  const int up = (1 << tb_log2) - 1;
-  PackedLevels l;
-  l.nb = (s.sq >> tb_log2) + ((s.sq & up) ? 1 : 0);
-  l.o = p.causal ? ((s.sk - s.sq) >> tb_log2) + (((s.sk - s.sq) & up) ? 1 : 0)
-                 : (s.sk >> tb_log2) + ((s.sk & up) ? 1 : 0);
-  return l;
-}
-
-// Blocks of the sequence at level q >= 0, and its next level below q (-1: none).
-__device__ __forceinline__ int blocks_at(const PackedLevels& l, int causal, int q) {
-  if (!causal) return q == l.o ? l.nb : 0;
-  if (q > 0) return (q >= l.o && q < l.o + l.nb) ? 1 : 0;   // o + nb <= 2^30 + 1: no sum wraps
-  return min(max(1 - l.o, 0), l.nb);
-}
-__device__ __forceinline__ int next_level(const PackedLevels& l, int causal, int q) {
-  if (l.nb == 0) return -1;
-  if (!causal) return l.o < q ? l.o : -1;
-  const int n = min(q - 1, max(l.o + l.nb - 1, 0));
-  return n >= max(l.o, 0) ? n : -1;
-}
-
-// The key-tile ranges of a packed item's query tiles (make_item's rule, in tokens).
-template <int BN>
-__device__ __forceinline__ void packed_ranges(const Params& p, Item& it) {
-  const int off = it.skv - it.sq;
-  const int tpt = BM >> p.pack_log2;   // tokens per tile
-  it.lo_all = 1 << 30;
-  it.hi_all = 0;
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const int r0 = it.q_row0 + tpt * i;
-    const int r1 = min(r0 + tpt, it.q_end);   // exclusive
-    int lo = 0, hi = 0;
-    if (r0 < r1) {
-      const int last_key = p.causal ? min(r1 - 1 + off, it.skv - 1) : it.skv - 1;
-      const int first_key = (p.causal && p.window > 0) ? max(0, r0 + off - p.window + 1) : 0;
-      if (last_key >= first_key) {
-        lo = first_key / BN;
-        hi = last_key / BN + 1;
-      }
-    }
-    it.lo[i] = lo;
-    it.hi[i] = hi;
-    if (hi > lo) {
-      it.lo_all = min(it.lo_all, lo);
-      it.hi_all = max(it.hi_all, hi);
-    }
-  }
-  if (it.hi_all <= 0) it.lo_all = it.hi_all = 0;
-}
-
-// Rows [from, to) of the item's last V tile lie behind its sequence and must be
-// zeroed before P V reads them (to <= from: none).  Dense rows behind a
-// sequence are the next one's; of paged ones only the box that holds the last
-// key brings any, since boxes wholly behind it are filled with zeros.
-template <int BN, bool PAGED>
-__device__ __forceinline__ void packed_v_tail(const Params& p, const Item& it, int& from, int& to) {
-  from = it.skv - (it.hi_all - 1) * BN;
-  to = BN;
-  if constexpr (PAGED) to = min(BN, (from + p.box_rows - 1) / p.box_rows * p.box_rows);
-}
-
 __device__ __forceinline__ bool active(const Item& it, int i, int j) { return j >= it.lo[i] && j < it.hi[i]; }
 
 // True if every (row, key) pair of query rows [r0, r0+BM) x key tile j is visible
@@ -321,22 +180,10 @@ __device__ __forceinline__ bool tile_unmasked(const Params& p, int skv, int r0, 
   return true;
 }
 
-// tile_unmasked for a packed item: query rows are the tokens [t0, t1] of the sequence.
-template <int BN>
-__device__ __forceinline__ bool packed_tile_unmasked(const Params& p, const Item& it, int t0, int t1, int j) {
-  const int off = it.skv - it.sq;
-  const int k0 = j * BN, k1 = j * BN + BN - 1;
-  if (k1 >= it.skv) return false;
-  if (!p.causal) return true;
-  if (k1 > t0 + off) return false;
-  if (p.window > 0 && k0 <= t1 + off - p.window) return false;
-  return true;
-}
-
 // PAGED selects K/V through a page table (chunked prefill over a paged cache)
 // instead of dense [B, Hkv, Skv, D] tensors; the dense kernel carries none of
-// the paged code.  PACKED: sequences of different lengths (see the head of this file).
-template <int D, bool PAGED, bool PACKED>
+// the paged code.
+template <int D, bool PAGED>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const Params p) {
@@ -360,14 +207,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   uint64_t* drain = s_free + NQ;                        // 1
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  // PACKED: the item ring, behind the 256 bytes of the barriers above
-  uint64_t* item_full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(bars) + 256);   // kItemRing
-  uint64_t* item_empty = item_full + kItemRing;         // kItemRing
-  uint64_t* tail_go = item_empty + kItemRing;           // 1: a V tile with rows to zero has landed
-  uint64_t* tail_done = tail_go + 1;                    // 1: they are zero
-  Item* item_ring = reinterpret_cast<Item*>(tail_done + 1);
-  static_assert(!PACKED || (2 * kItemRing + 2) * 8 + kItemRing * sizeof(Item) <= kPackedSmem, "item ring");
-  static_assert((2 * QBUF + 2 * STAGES + 4 * NQ + 1) * 8 + 8 <= 256, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n_rounds = (p.n_items + gridDim.x - 1) / gridDim.x;
@@ -388,14 +227,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       mbar_init(&s_free[i], 4 * 32);
     }
     mbar_init(drain, 1);
-    if constexpr (PACKED) {
-      for (int s = 0; s < kItemRing; ++s) {
-        mbar_init(&item_full[s], 1);
-        mbar_init(&item_empty[s], kItemConsumers);
-      }
-      mbar_init(tail_go, 1);
-      mbar_init(tail_done, 32);
-    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -409,19 +240,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   // set-up above overlaps the tail of the kernel before; global memory only from here on
   grid_dependency_wait();
-
-  // PACKED: the r-th item from the scheduler's ring; false at the end of the list or
-  // if a wait gave up.  whole_warp: all 32 lanes call (one lane arrives for them).
-  auto next_item = [&](int r, bool whole_warp, Item& it) -> bool {
-    const int slot = r % kItemRing;
-    bool got = mbar_wait(&item_full[slot], (r / kItemRing) & 1, abort_flag, p.err);
-    if (whole_warp) got = __all_sync(0xffffffffu, got);
-    if (!got) return false;
-    it = item_ring[slot];
-    if (whole_warp) __syncwarp();
-    if (!whole_warp || lane == 0) mbar_arrive(&item_empty[slot]);
-    return it.b >= 0;
-  };
 
   if (warp >= 8) {
    // ------------------------------------------------------------ producer warpgroup
@@ -444,28 +262,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       int n = 0, qn = 0;
       bool ok = true;
-      for (int r = 0; (PACKED || r < n_rounds) && ok; ++r) {
-        Item it;
-        if constexpr (PACKED) {
-          if (!next_item(r, PAGED, it)) break;
-        } else {
-          const int k = item_index(p, r);
-          if (k < 0) continue;
-          it = make_item<BN, PAGED>(p, k);
-        }
+      for (int r = 0; r < n_rounds && ok; ++r) {
+        const int k = item_index(p, r);
+        if (k < 0) continue;
+        const Item it = make_item<BN, PAGED>(p, k);
         if (it.hi_all <= it.lo_all) continue;
         const int qb = qn % QBUF;
         if (qn >= QBUF && !(ok = uni(mbar_wait(&q_empty[qb], ((qn / QBUF) - 1) & 1, abort_flag, p.err)))) break;
-        if (PACKED && lead) {
-          // a tile without tokens is not loaded; nothing multiplies it either
-          const int tpt = BM >> p.pack_log2;
-          const int nt = (it.q_row0 + tpt < it.q_end) ? NQ : 1;
-          mbar_arrive_expect_tx(&q_full[qb], nt * C::Q_BYTES);
-          for (int i = 0; i < nt; ++i)
-            for (int a = 0; a < C::KATOMS; ++a)
-              tma_load_4d(sQ + ((qb * NQ + i) * C::KATOMS + a) * BM * 128, &tmap_q, &q_full[qb], a * 64, 0,
-                          it.q_base + it.q_row0 + tpt * i, it.bh);
-        } else if (lead) {
+        if (lead) {
           mbar_arrive_expect_tx(&q_full[qb], NQ * C::Q_BYTES);
           for (int i = 0; i < NQ; ++i)
             for (int a = 0; a < C::KATOMS; ++a)
@@ -473,8 +277,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
                           it.q_row0 + BM * i, it.bh);
         }
         ++qn;
-        const int kv_plane = PACKED ? it.g : it.b * p.Hkv + it.g;
-        const int kv_row0 = PACKED ? it.k_base : 0;
+        const int kv_plane = it.b * p.Hkv + it.g;
         // PAGED: the physical page of this lane's box of key tile j (lane rb + nb * a
         // copies box rb of swizzle atom a), or the pool size for a box past the end
         // of the sequence.  K_j and V_j share it, and it is read one tile ahead, so
@@ -505,8 +308,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           const CUtensorMap* tm = is_v ? &tmap_v : &tmap_k;
           if constexpr (!PAGED) {
             for (int a = 0; a < C::KATOMS; ++a)
-              tma_load_3d(sRing + st * C::TILE_BYTES + a * BN * 128, tm, &full[st], a * 64, kv_row0 + j * BN,
-                          kv_plane);
+              tma_load_3d(sRing + st * C::TILE_BYTES + a * BN * 128, tm, &full[st], a * 64, j * BN, kv_plane);
           } else {
             // the key tile is assembled from page boxes of box_rows rows each; a
             // box lands at its row offset inside the swizzled tile, so the MMA
@@ -583,27 +385,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // and P is 0 there, but 0 * NaN is NaN, so the V rows past the end are
       // zeroed in shared memory before P.V reads them.  Boxes wholly past the
       // end arrive as zeros already.
-      // PACKED: warp 11 does it, while the softmax of this tile runs (tail_go / tail_done).
-      int tails = 0;
-      auto v_tail_start = [&](const Item& it, int j) -> bool {
-        if constexpr (!PACKED) return false;
-        if (j != it.hi_all - 1) return false;
-        int from, to;
-        packed_v_tail<BN, PAGED>(p, it, from, to);
-        if (to <= from) return false;
-        mbar_arrive(tail_go);
-        return true;
-      };
-      auto v_tail_wait = [&](bool& pending) -> bool {
-        if constexpr (!PACKED) return true;
-        if (!pending) return true;
-        pending = false;
-        const bool r = mbar_wait(tail_done, tails & 1, abort_flag, p.err);
-        ++tails;
-        return r;
-      };
       auto clear_v_tail = [&](int st, int j, int skv) {
-        if constexpr (!PAGED || PACKED) return;
+        if constexpr (!PAGED) return;
         const int from = skv - j * BN;
         if (from <= 0 || from >= BN) return;
         const int to = min(BN, (from + p.box_rows - 1) / p.box_rows * p.box_rows);
@@ -629,15 +412,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         // Order per key tile j: S_i(j+1) as soon as softmax group i has loaded
         // S_i(j) (s_free), then P_i(j) V_j as soon as it has written P_i(j).
         int tf[NQ] = {0, 0};    // s_free phases consumed per tile
-        for (int r = 0; (PACKED || r < n_rounds) && ok; ++r) {
-          Item it;
-          if constexpr (PACKED) {
-            if (!next_item(r, false, it)) break;
-          } else {
-            const int k = item_index(p, r);
-            if (k < 0) continue;
-            it = make_item<BN, PAGED>(p, k);
-          }
+        for (int r = 0; r < n_rounds && ok; ++r) {
+          const int k = item_index(p, r);
+          if (k < 0) continue;
+          const Item it = make_item<BN, PAGED>(p, k);
           if (it.hi_all <= it.lo_all) continue;
           const int qb = qn % QBUF;
           if (!(ok = mbar_wait(&q_full[qb], (qn / QBUF) & 1, abort_flag, p.err))) break;
@@ -672,13 +450,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             int stV;
             if (!(ok = wait_slot(stV))) break;
             clear_v_tail(stV, j, it.skv);
-            bool tail = v_tail_start(it, j);
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
               if (!active(it, i, j)) continue;
               if (!(ok = mbar_wait(&p_ready[i], ts[i] & 1, abort_flag, p.err))) break;
-              ok = v_tail_wait(tail);
-              if (!ok) break;
               tc_fence_after();
               ++ts[i];
               const uint32_t o_tmem = tmem + C::O_COL + D * i;
@@ -704,15 +479,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           }
         }
       } else {
-      for (int r = 0; (PACKED || r < n_rounds) && ok; ++r) {
-          Item it;
-          if constexpr (PACKED) {
-            if (!next_item(r, false, it)) break;
-          } else {
-            const int k = item_index(p, r);
-            if (k < 0) continue;
-            it = make_item<BN, PAGED>(p, k);
-          }
+      for (int r = 0; r < n_rounds && ok; ++r) {
+          const int k = item_index(p, r);
+          if (k < 0) continue;
+          const Item it = make_item<BN, PAGED>(p, k);
           if (it.hi_all <= it.lo_all) continue;
           const int qb = qn % QBUF;
           if (!(ok = mbar_wait(&q_full[qb], (qn / QBUF) & 1, abort_flag, p.err))) break;
@@ -731,15 +501,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             int stV;
             if (!(ok = wait_slot(stV))) break;
             clear_v_tail(stV, j, it.skv);
-            bool tail = v_tail_start(it, j);
             const bool next = j + 1 < it.hi_all;
             int stK1 = -1;
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
               if (active(it, i, j)) {
                 if (!(ok = mbar_wait(&p_ready[i], ts[i] & 1, abort_flag, p.err))) break;
-                ok = v_tail_wait(tail);
-                if (!ok) break;
                 tc_fence_after();
                 ++ts[i];
                 const uint32_t o_tmem = tmem + C::O_COL + D * i;
@@ -768,121 +535,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // everything issued above must be complete before tensor memory is released
       mma_commit(drain);
       mbar_wait(drain, 0, nullptr, p.err);
-    }
-   } else if (PACKED && warp == kSchedWarp) {
-    // ------------------------------------------------------------ item scheduler (PACKED)
-    // Blocks are ranked level by level from the highest (costliest) down, within
-    // a level by sequence; item k is head block k % head_blocks of the block of
-    // rank k / head_blocks.  This CTA's k only grow, so one walk down the levels
-    // serves all its items; a level costs a pass over the sequences, 32 at a time.
-    const int tpt = BM >> p.pack_log2;
-    const int tb_log2 = 7 - p.pack_log2 + (p.tiles - 1);
-    const int chunks = (p.B + 31) / 32;
-    PackedLevels first = {0, 0};
-    if (lane < p.B) first = packed_levels<PAGED>(p, lane, tb_log2);
-    auto levels_of = [&](int c) -> PackedLevels {   // sequence 32 c + lane
-      if (c == 0) return first;
-      PackedLevels l = {0, 0};
-      if (c * 32 + lane < p.B) l = packed_levels<PAGED>(p, c * 32 + lane, tb_log2);
-      return l;
-    };
-    int level = 0x7FFFFFFF, below = -1, base = 0, count = 0;
-    auto visit = [&](int q) {   // blocks at level q, and the next level that has any
-      int m = 0, nx = -1;
-      for (int c = 0; c < chunks; ++c) {
-        const PackedLevels l = levels_of(c);
-        m += blocks_at(l, p.causal, q);
-        nx = max(nx, next_level(l, p.causal, q));
-      }
-      level = q;
-      count = __reduce_add_sync(0xffffffffu, m);
-      below = __reduce_max_sync(0xffffffffu, nx);
-    };
-    visit(0x7FFFFFFF);   // above every level: no blocks
-    for (int r = 0;; ++r) {
-      const int slot = r % kItemRing;
-      if (!__all_sync(0xffffffffu, mbar_wait(&item_empty[slot], ((r / kItemRing) & 1) ^ 1, abort_flag, p.err))) break;
-      const int P = gridDim.x, c = blockIdx.x;
-      const int k = r * P + ((r & 1) ? (P - 1 - c) : c);
-      const int rank = k / p.head_blocks;
-      while (level >= 0 && rank >= base + count) {
-        base += count;
-        if (below < 0) level = -1;
-        else visit(below);
-      }
-      Item it;
-      it.b = -1;
-      // sequences that do not overlap have at most n_items items: more means malformed lengths
-      if (level >= 0 && k >= p.n_items) {
-        if (lane == 0) record_error(p.err, ATTN_ERRBIT_BADPAGE);
-        level = -1;
-      }
-      if (level >= 0) {
-        int j = rank - base;   // the j-th block of this level
-        for (int ch = 0; ch < chunks; ++ch) {
-          const PackedLevels l = levels_of(ch);
-          const int m = blocks_at(l, p.causal, level);
-          int incl = m;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += v;
-          }
-          const int total = __shfl_sync(0xffffffffu, incl, 31);
-          if (j >= total) {
-            j -= total;
-            continue;
-          }
-          const int src = __ffs(__ballot_sync(0xffffffffu, incl > j)) - 1;
-          j -= __shfl_sync(0xffffffffu, incl - m, src);
-          const int o = __shfl_sync(0xffffffffu, l.o, src), nb = __shfl_sync(0xffffffffu, l.nb, src);
-          const int qb = (p.causal && level > 0) ? level - o : j;
-          // (counts of malformed, overlapping lengths may have wrapped: no block then)
-          if (src < 0 || ch * 32 + src >= p.B || qb < 0 || qb >= nb) break;
-          it.b = ch * 32 + src;
-          const PackedSpan s = packed_span<PAGED>(p, it.b);
-          it.bh = k - rank * p.head_blocks;
-          it.g = (it.bh << p.pack_log2) / (p.Hq / p.Hkv);
-          it.q_row0 = qb << tb_log2;
-          it.q_end = min(s.sq, it.q_row0 + p.tiles * tpt);
-          it.q_base = s.q0;
-          it.k_base = s.k0;
-          it.sq = s.sq;
-          it.skv = s.sk;
-          packed_ranges<BN>(p, it);
-          break;
-        }
-      }
-      if (lane == 0) {
-        item_ring[slot] = it;
-        mbar_arrive(&item_full[slot]);
-      }
-      if (it.b < 0) break;
-    }
-   } else if (PACKED && warp == kTailWarp) {
-    // ------------------------------------------------------------ V rows behind a sequence (PACKED)
-    int n = 0, tails = 0;   // ring loads of the items so far (K and V of each key tile), tiles zeroed
-    for (int r = 0;; ++r) {
-      Item it;
-      if (!next_item(r, true, it)) break;
-      if (it.hi_all <= it.lo_all) continue;
-      n += 2 * (it.hi_all - it.lo_all);   // the last V tile is the item's last load
-      int from, to;
-      packed_v_tail<BN, PAGED>(p, it, from, to);
-      if (to <= from) continue;
-      const int st = (n - 1) % STAGES;
-      // the MMA thread has seen the tile land, and frees its slot only after tail_done
-      bool got = mbar_wait(tail_go, tails & 1, abort_flag, p.err);
-      got = got && mbar_wait(&full[st], ((n - 1) / STAGES) & 1, abort_flag, p.err);
-      if (!__all_sync(0xffffffffu, got)) break;
-      ++tails;
-      for (int a = 0; a < C::KATOMS; ++a) {
-        const uint32_t rows = smem_u32(sRing + st * C::TILE_BYTES + a * BN * 128);
-        for (int e = from * 128 + lane * 16; e < to * 128; e += 512)   // a row holds its key's values under the swizzle
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(rows + e), "r"(0u) : "memory");
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(tail_done);
     }
    }
   } else {
@@ -919,42 +571,27 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     };
     bool ok = true;
 
-    for (int rr = 0; (PACKED || rr < n_rounds) && ok; ++rr) {
-      Item it;
-      if constexpr (PACKED) {
-        if (!next_item(rr, true, it)) break;
-      } else {
-        const int k = item_index(p, rr);
-        if (k < 0) continue;
-        it = make_item<BN, PAGED>(p, k);
-      }
+    for (int rr = 0; rr < n_rounds && ok; ++rr) {
+      const int k = item_index(p, rr);
+      if (k < 0) continue;
+      const Item it = make_item<BN, PAGED>(p, k);
       const int my_lo = (i == 0) ? it.lo[0] : it.lo[1];
       const int my_hi = (i == 0) ? it.hi[0] : it.hi[1];
-      // query row of this thread; PACKED: a token of the sequence, one of 2^s heads
-      const int r0 = it.q_row0 + (PACKED ? BM >> p.pack_log2 : BM) * i;
-      const int r = r0 + (PACKED ? rl >> p.pack_log2 : rl);
-      const bool store = PACKED ? r < it.q_end : r < p.Sq;
-      auto head = [&]() -> int { return (it.bh << p.pack_log2) + (rl & ((1 << p.pack_log2) - 1)); };   // PACKED
-      auto lse_at = [&]() -> size_t {
-        if constexpr (PACKED) return (static_cast<size_t>(it.q_base) + r) * p.Hq + head();
-        else return static_cast<size_t>(it.bh) * p.Sq + r;
-      };
-      __nv_bfloat16* orow;
-      if constexpr (PACKED)
-        orow = p.out + (static_cast<size_t>(it.q_base) + r) * p.out_stride + static_cast<size_t>(head()) * D;
-      else
-        orow = p.out + (static_cast<size_t>(it.bh) * p.Sq + r) * D;
+      const int r0 = it.q_row0 + BM * i;
+      const int r = r0 + rl;                 // query row of this thread
+      const bool store = r < p.Sq;
+      __nv_bfloat16* orow = p.out + (static_cast<size_t>(it.bh) * p.Sq + r) * D;
       if (my_hi <= my_lo) {                  // no visible key for any row of this tile
         if (store) {
           uint4* dst = reinterpret_cast<uint4*>(orow);
           for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
-          if (p.lse != nullptr) p.lse[lse_at()] = -INFINITY;
+          if (p.lse != nullptr) p.lse[static_cast<size_t>(it.bh) * p.Sq + r] = -INFINITY;
         }
         continue;
       }
       // visible keys of this row: [key_lo, key_hi]
       const int skv = it.skv;
-      const int off = skv - (PACKED ? it.sq : p.Sq);
+      const int off = skv - p.Sq;
       const int key_hi = p.causal ? min(r + off, skv - 1) : skv - 1;
       const int key_lo = (p.causal && p.window > 0) ? r + off - p.window + 1 : 0;
       float m_ref = -INFINITY, l = 0.f;
@@ -974,10 +611,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           tc_fence_before();
           mbar_arrive(&s_free[i]);
         }
-        bool masked;
-        if constexpr (PACKED) masked = !packed_tile_unmasked<BN>(p, it, r0, r0 + (BM >> p.pack_log2) - 1, j);
-        else masked = !tile_unmasked<BN>(p, skv, r0, j);
-        if (masked) {
+        if (!tile_unmasked<BN>(p, skv, r0, j)) {
           const int c_lo = key_lo - j * BN, c_hi = key_hi - j * BN;
 #pragma unroll
           for (int c = 0; c < BN; ++c) s[c] = (c >= c_lo && c <= c_hi) ? s[c] : -INFINITY;
@@ -1058,7 +692,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const bool has_keys = key_hi >= max(key_lo, 0);
       const float inv = (has_keys && l > 0.f) ? 1.f / l : 0.f;
       if (p.lse != nullptr && store)   // log(sum_j exp(s_ij * scale)) = (m + log2 l) * ln 2
-        p.lse[lse_at()] =
+        p.lse[static_cast<size_t>(it.bh) * p.Sq + r] =
             (has_keys && l > 0.f) ? (m_ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1113,22 +747,16 @@ EncodeTiledFn tensor_map_encoder() {
 }
 }  // namespace
 
-namespace {
-
-// Tensor map over `rank` (3 or 4) dimensions, innermost first: 128-byte swizzle, zeros out of bounds.
-// strides: bytes between elements of dimensions 1 .. rank - 1.
-bool encode_map(CUtensorMap* m, const void* base, int elem_bytes, int rank, const cuuint64_t* dims,
-                const cuuint64_t* strides, const cuuint32_t* box) {
+bool encode_tensor_map(CUtensorMap* m, const void* base, int elem_bytes, int rank, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn enc = tensor_map_encoder();
-  if (enc == nullptr || (elem_bytes != 1 && elem_bytes != 2)) return false;
+  if (enc == nullptr || (elem_bytes != 1 && elem_bytes != 2) || rank > 4) return false;
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(m, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-}  // namespace
 
 bool make_tensor_map_3d(CUtensorMap* m, const void* base, int elem_bytes, int inner, int rows, int planes,
                         int box_inner, int box_rows) {
@@ -1137,7 +765,7 @@ bool make_tensor_map_3d(CUtensorMap* m, const void* base, int elem_bytes, int in
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner) * elem_bytes,
                                  static_cast<cuuint64_t>(rows) * inner * elem_bytes};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows), 1};
-  return encode_map(m, base, elem_bytes, 3, dims, strides, box);
+  return encode_tensor_map(m, base, elem_bytes, 3, dims, strides, box);
 }
 
 namespace {
@@ -1145,27 +773,6 @@ namespace {
 // [planes][rows][D] bf16 tensor, boxes of 64 columns x box_rows rows, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const void* base, int D, int rows, int planes, int box_rows = 128) {
   return make_tensor_map_3d(m, base, 2, D, rows, planes, 64, box_rows);
-}
-
-// Packed q: [tokens][head blocks of 2^s][D] bf16 rows `stride` elements apart, as
-// (column, head of the block, token, head block); a box is one query tile.
-bool make_map_packed_q(CUtensorMap* m, const void* base, int D, int tokens, int head_blocks, int pack_log2,
-                       long long stride) {
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), 1ull << pack_log2, static_cast<cuuint64_t>(tokens),
-                              static_cast<cuuint64_t>(head_blocks)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2,
-                                 (static_cast<cuuint64_t>(D) << pack_log2) * 2};
-  const cuuint32_t box[4] = {64, 1u << pack_log2, static_cast<cuuint32_t>(BM >> pack_log2), 1};
-  return encode_map(m, base, 2, 4, dims, strides, box);
-}
-
-// Packed k or v: [tokens][Hkv][D] bf16 rows `stride` elements apart, as (column, token, head).
-bool make_map_packed_kv(CUtensorMap* m, const void* base, int D, int tokens, int Hkv, long long stride, int box_rows) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(tokens),
-                              static_cast<cuuint64_t>(Hkv)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride) * 2, static_cast<cuuint64_t>(D) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-  return encode_map(m, base, 2, 3, dims, strides, box);
 }
 
 }  // namespace
@@ -1190,7 +797,7 @@ namespace {
 // block's own registers cover the request, so a build whose launch
 // allocation could not is refused).  Done once per device; later calls skip
 // the runtime queries, which cost more host time than the launch itself.
-template <int D, bool PAGED, bool PACKED>
+template <int D, bool PAGED>
 cudaError_t prepare_kernel() {
   using C = Cfg<D>;
   constexpr int kMaxDevices = 64;
@@ -1198,9 +805,8 @@ cudaError_t prepare_kernel() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE) == 1) return cudaSuccess;
-  auto kern = prefill_tc_kernel<D, PAGED, PACKED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(C::SMEM + (PACKED ? kPackedSmem : 0)));
+  auto kern = prefill_tc_kernel<D, PAGED>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
   cudaFuncAttributes fa{};
   e = cudaFuncGetAttributes(&fa, kern);
@@ -1211,13 +817,13 @@ cudaError_t prepare_kernel() {
   return cudaSuccess;
 }
 
-template <int D, bool PAGED, bool PACKED = false>
+template <int D, bool PAGED>
 cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p,
                      cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kern = prefill_tc_kernel<D, PAGED, PACKED>;
-  const size_t smem = C::SMEM + (PACKED ? kPackedSmem : 0);
-  cudaError_t e = prepare_kernel<D, PAGED, PACKED>();
+  auto kern = prefill_tc_kernel<D, PAGED>;
+  const size_t smem = C::SMEM;
+  cudaError_t e = prepare_kernel<D, PAGED>();
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
@@ -1287,88 +893,6 @@ cudaError_t launch_prefill_tc_paged(const void* q, const void* k_pool, const voi
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   return D == 64 ? launch_d<64, true>(mq, mk, mv, p, stream) : launch_d<128, true>(mq, mk, mv, p, stream);
-}
-
-namespace {
-
-// What the packed launches share: the head packing, the item bound that sizes the
-// grid, and the fields of Params that do not depend on where K and V lie.
-bool packed_params(Params& p, const void* out, float* lse, const int32_t* cu_q, int B, int Hq, int Hkv, int Tq,
-                   long long out_stride, float scale, int causal, int window, unsigned int* err) {
-  p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.Tq = Tq;
-  p.causal = causal;
-  p.window = window;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out));
-  p.lse = lse;
-  p.err = err;
-  p.cu_q = cu_q;
-  p.out_stride = out_stride;
-  int s = 0;
-  while (s < 7 && ((Hq / Hkv) & (1 << s)) == 0) ++s;   // 2^s divides the group, at most 128 heads
-  p.pack_log2 = s;
-  p.head_blocks = Hq >> s;
-  p.tiles = 2;
-  // sequences of any lengths make at most Tq / block + B blocks; items are counted in int32,
-  // with room for one more round of the grid
-  const int block = (BM >> s) * p.tiles;
-  const long long items = (static_cast<long long>(Tq) / block + B) * p.head_blocks;
-  if (items > (1LL << 30)) return false;
-  p.n_items = static_cast<int>(items);
-  return true;
-}
-
-}  // namespace
-
-cudaError_t launch_prefill_tc_packed(const void* q, const void* k, const void* v, const int32_t* cu_q,
-                                     const int32_t* cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int D,
-                                     long long q_stride, long long k_stride, long long v_stride, long long out_stride,
-                                     float scale, int causal, int window, void* out, float* lse, unsigned int* err,
-                                     cudaStream_t stream) {
-  Params p{};
-  if (!packed_params(p, out, lse, cu_q, B, Hq, Hkv, Tq, out_stride, scale, causal, window, err))
-    return cudaErrorNotSupported;
-  p.cu_k = cu_k;
-  p.Tk = Tk;
-  const int bn = (D == 64) ? Cfg<64>::BN : Cfg<128>::BN;
-  CUtensorMap mq, mk, mv;
-  // without keys the k and v maps are never used: any valid address will do
-  const void* kb = Tk > 0 ? k : q;
-  const void* vb = Tk > 0 ? v : q;
-  const int rows = Tk > 0 ? Tk : 1;
-  if (!make_map_packed_q(&mq, q, D, Tq, p.head_blocks, p.pack_log2, q_stride) ||
-      !make_map_packed_kv(&mk, kb, D, rows, Hkv, k_stride, bn) || !make_map_packed_kv(&mv, vb, D, rows, Hkv, v_stride, bn))
-    return cudaErrorInvalidValue;
-  return D == 64 ? launch_d<64, false, true>(mq, mk, mv, p, stream) : launch_d<128, false, true>(mq, mk, mv, p, stream);
-}
-
-cudaError_t launch_prefill_tc_packed_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* cu_q,
-                                           const int32_t* page_table, const int32_t* seq_lens, int page_size, int B,
-                                           int Tq, int Hq, int Hkv, int D, long long q_stride, long long out_stride,
-                                           int num_pages, int max_pages, int max_seq_len, float scale, int causal,
-                                           int window, void* out, float* lse, unsigned int* err, cudaStream_t stream) {
-  Params p{};
-  if (!packed_params(p, out, lse, cu_q, B, Hq, Hkv, Tq, out_stride, scale, causal, window, err))
-    return cudaErrorNotSupported;
-  const int bn = (D == 64) ? Cfg<64>::BN : Cfg<128>::BN;
-  p.Skv = max_seq_len;
-  p.page_table = page_table;
-  p.seq_lens = seq_lens;
-  p.page_size = page_size;
-  p.box_rows = page_size < bn ? page_size : bn;
-  p.max_pages = max_pages;
-  p.num_pages = num_pages;
-  CUtensorMap mq, mk, mv;
-  // with max_seq_len 0 nothing is cached and the pools' maps are never used
-  const bool any = max_seq_len > 0;
-  if (!make_map_packed_q(&mq, q, D, Tq, p.head_blocks, p.pack_log2, q_stride) ||
-      !make_map(&mk, any ? k_pool : q, D, page_size, any ? num_pages * Hkv : 1, p.box_rows) ||
-      !make_map(&mv, any ? v_pool : q, D, page_size, any ? num_pages * Hkv : 1, p.box_rows))
-    return cudaErrorInvalidValue;
-  return D == 64 ? launch_d<64, true, true>(mq, mk, mv, p, stream) : launch_d<128, true, true>(mq, mk, mv, p, stream);
 }
 
 }  // namespace attn

@@ -93,6 +93,24 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return mbar_wait_for(bar, parity, abort, err, ATTN_WAIT_NS);
 }
 
+// mbar_wait for a role that has long waits and no haste: it sleeps between
+// polls, so that it takes no issue slots from the warps that work.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                               unsigned int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (abort != nullptr && *abort) return false;
+    if (globaltimer_ns() - t0 > ATTN_WAIT_NS) {
+      record_error(err, ATTN_ERRBIT_TIMEOUT);
+      if (abort != nullptr) *abort = 1;
+      return false;
+    }
+    __nanosleep(200);
+  }
+  return true;
+}
+
 // ----------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
