@@ -22,13 +22,17 @@
 // costliest (last visible key farthest) down, deals them out in a snake over
 // the CTAs, and hands each to the other roles through a ring in shared memory.
 // Nothing is stored in memory and no other launch precedes this one.
-// Stages.  The key tiles of all of a CTA's items form one stream.  Stage g
-// holds V of tile g - 1 and K of tile g, because the MMA thread uses them
-// together: P V of one tile, then S of the next, for query tile 0 and then 1
-// (D = 128), so one full and one empty barrier serve two loads, and the next
-// item's first K comes with the last V of the item before.  That thread's own
-// instructions are what paces D = 128 (about 90 cycles go by per MMA and 160
-// per wait, also for one already complete; 32 MMAs and 4 waits a key tile).
+// Stages, D = 128.  The key tiles of all of a CTA's items form one stream.
+// Stage g holds V of tile g - 1 and K of tile g, because the MMA thread uses
+// them together: P V of one tile, then S of the next, for query tile 0 and then
+// 1.  One full and one empty barrier serve two loads, and the next item's first
+// K comes with the last V of the item before.  That thread's own instructions
+// are what paces D = 128 (it never waits for a P in a long item: about 60 cycles
+// go by per MMA, 100 per wait, also for one already complete, and 40 to 60 per
+// commit, 2980 a key tile, of which the products themselves need 2048); with
+// a barrier for each load it took 5 % longer.
+// At D = 64 a stage is a single K or V tile: S_i(j + 1) runs ahead of P_i(j) V_j, and
+// would only wait longer for a V that it does not need (6 % on items of 2 key tiles).
 // Tail.  The last key tile of a sequence is followed in memory by the next
 // sequence's rows (or by whatever the page holds).  Their scores are masked
 // like any others; the V rows are zeroed in shared memory (0 * NaN is NaN) by
@@ -72,8 +76,8 @@ struct Cfg {
   static constexpr int TILE_BYTES = BN * D * 2;       // one K or V tile
   static constexpr int Q_BYTES = BM * D * 2;          // one query tile
   static constexpr int QBUF = (D == 128) ? 1 : 2;     // query buffers (items in flight)
-  static constexpr int STAGES = (D == 128) ? 2 : 4;   // of a V and a K tile each
-  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // V, then K
+  static constexpr int STAGES = (D == 128) ? 2 : 8;
+  static constexpr int STAGE_BYTES = (D == 128) ? 2 * TILE_BYTES : TILE_BYTES;   // V, then K; one tile
   static constexpr bool SEP_P = (D == 64);            // P has tensor memory of its own
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t S_COL = 0;                // + BN * i
@@ -155,9 +159,7 @@ struct PackedLevels {
   int o, nb;
 };
 
-template <bool PAGED>
-__device__ __forceinline__ PackedLevels packed_levels(const Params& p, int b, int tb_log2) {
-  const PackedSpan s = packed_span<PAGED>(p, b);
+__device__ __forceinline__ PackedLevels packed_levels(const Params& p, const PackedSpan& s, int tb_log2) {
   const int up = (1 << tb_log2) - 1;
   PackedLevels l;
   l.nb = (s.sq >> tb_log2) + ((s.sq & up) ? 1 : 0);
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;                                   // [QBUF][NQ][KATOMS][BM rows x 128 B]
-  uint8_t* sRing = smem + QBUF * NQ * C::Q_BYTES;       // [STAGES][V, K][KATOMS][BN rows x 128 B]
+  uint8_t* sRing = smem + QBUF * NQ * C::Q_BYTES;       // [STAGES][one tile, or V and K][KATOMS][BN rows x 128 B]
   uint8_t* control = sRing + STAGES * C::STAGE_BYTES;
   uint8_t* sOut = control + C::CONTROL;                 // [8 softmax warps][4 KB]
   uint64_t* q_full = reinterpret_cast<uint64_t*>(control);   // QBUF
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           }
         }
       };
-      // next stage <- V of tile vj of v (unless null) and K of tile kj of k (unless null)
+      // next stage <- V of tile vj of v (unless null), then K of tile kj of k (unless null)
       auto load_stage = [&](const Item* v, int vj, int vph, const Item* k, int kj, int kph) -> bool {
         const int st = n % STAGES;
         if (!uni(mbar_wait(&empty[st], ((n / STAGES) & 1) ^ 1, abort_flag, p.err))) return false;
@@ -408,37 +410,55 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if constexpr (PAGED) __syncwarp();   // the barrier is armed before any box can land
         uint8_t* dst = sRing + st * C::STAGE_BYTES;
         if (v) copy_tile(dst, &tmap_v, &full[st], *v, vj, vph);
-        if (k) copy_tile(dst + C::TILE_BYTES, &tmap_k, &full[st], *k, kj, kph);
+        if (k) copy_tile(dst + (C::SEP_P ? 0 : C::TILE_BYTES), &tmap_k, &full[st], *k, kj, kph);
         ++n;
         return true;
       };
-      Item it, nx;
+      Item it;
       bool have = next_work(r, PAGED, it);
-      int ph = 0;
-      if (have) {
-        ph = page_of(it, it.lo_all);
-        ok = load_stage(nullptr, 0, 0, &it, it.lo_all, ph);
-      }
-      while (have && ok) {
-        // Q waits for the S of an item before; the item's first K went ahead of it
-        if (!(ok = load_q(it))) break;
-        bool more = false;
-        int ph1 = (it.lo_all + 1 < it.hi_all) ? page_of(it, it.lo_all + 1) : 0;
-        for (int j = it.lo_all; j < it.hi_all && ok; ++j) {
-          if (j + 1 < it.hi_all) {
+      // load order = the MMA thread's consumption order
+      if constexpr (C::SEP_P) {   // Q, K_lo, then K_{j+1} ahead of V_j
+        while (have && ok) {
+          int ph = page_of(it, it.lo_all);
+          int ph1 = (it.lo_all + 1 < it.hi_all) ? page_of(it, it.lo_all + 1) : 0;
+          ok = load_q(it) && load_stage(nullptr, 0, 0, &it, it.lo_all, ph);
+          for (int j = it.lo_all; j < it.hi_all && ok; ++j) {
             const int ph2 = (j + 2 < it.hi_all) ? page_of(it, j + 2) : 0;
-            ok = load_stage(&it, j, ph, &it, j + 1, ph1);
+            if (j + 1 < it.hi_all) ok = load_stage(nullptr, 0, 0, &it, j + 1, ph1);
+            if (ok) ok = load_stage(&it, j, ph, nullptr, 0, 0);
             ph = ph1;
             ph1 = ph2;
-          } else {
-            more = next_work(r, PAGED, nx);
-            const int phn = more ? page_of(nx, nx.lo_all) : 0;
-            ok = load_stage(&it, j, ph, more ? &nx : nullptr, more ? nx.lo_all : 0, phn);
-            ph = phn;
           }
+          if (ok) have = next_work(r, PAGED, it);
         }
-        it = nx;
-        have = more;
+      } else {                    // K_lo, Q, then V_j with K_{j+1} or the next item's first K
+        Item nx;
+        int ph = 0;
+        if (have) {
+          ph = page_of(it, it.lo_all);
+          ok = load_stage(nullptr, 0, 0, &it, it.lo_all, ph);
+        }
+        while (have && ok) {
+          // Q waits for the S of the item before; this item's first K went ahead of it
+          if (!(ok = load_q(it))) break;
+          bool more = false;
+          int ph1 = (it.lo_all + 1 < it.hi_all) ? page_of(it, it.lo_all + 1) : 0;
+          for (int j = it.lo_all; j < it.hi_all && ok; ++j) {
+            if (j + 1 < it.hi_all) {
+              const int ph2 = (j + 2 < it.hi_all) ? page_of(it, j + 2) : 0;
+              ok = load_stage(&it, j, ph, &it, j + 1, ph1);
+              ph = ph1;
+              ph1 = ph2;
+            } else {
+              more = next_work(r, PAGED, nx);
+              const int phn = more ? page_of(nx, nx.lo_all) : 0;
+              ok = load_stage(&it, j, ph, more ? &nx : nullptr, more ? nx.lo_all : 0, phn);
+              ph = phn;
+            }
+          }
+          it = nx;
+          have = more;
+        }
       }
       if (ok) pass_rest(r, PAGED, it);
       // the last loads issued must land before the CTA may exit (normally already consumed)
@@ -454,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // blocks BN * 128 bytes apart); a K step adds a compile-time offset in 16-byte units
       const uint32_t q_lo0 = sw128_desc_lo(smem_u32(sQ), 16);
       const uint32_t v_lo0 = sw128_desc_lo(smem_u32(sRing), BN * 128);
-      const uint32_t k_lo0 = sw128_desc_lo(smem_u32(sRing) + C::TILE_BYTES, 16);
+      const uint32_t k_lo0 = sw128_desc_lo(smem_u32(sRing) + (C::SEP_P ? 0 : C::TILE_BYTES), 16);
       int r = 0, n = 0, qn = 0, tails = 0;
       uint32_t tp = 0;          // bit i: parity of P_i's next phase
       bool ok = true;
@@ -503,12 +523,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         return got;
       };
 
-      Item it, nx;
+      Item it;
       bool have = next_work(r, false, it);
-      if (have) ok = wait_stage(0);
       if constexpr (C::SEP_P) {
-        // Per key tile j: S_i(j + 1), or S_i of the next item's first tile, as soon as softmax group i has
-        // loaded the S_i before it (s_free), then P_i(j) V_j as soon as it has written P_i(j).
+        // Per key tile j: S_i(j + 1) as soon as softmax group i has loaded S_i(j) (s_free), then
+        // P_i(j) V_j as soon as it has written P_i(j).
         uint32_t used = 0, tf = 0;   // bit i: S_i was written before; parity of s_free's next phase
         auto issue_next_s = [&](int i, int qb, int st) -> bool {
           if (used & (1u << i)) {
@@ -520,45 +539,35 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           issue_s(i, qb, st);
           return true;
         };
-        auto wait_q = [&]() -> bool {
+        while (have && ok) {
           const int qb = qn % QBUF;
-          const bool got = mbar_wait(&q_full[qb], (qn / QBUF) & 1, abort_flag, p.err);
+          if (!(ok = mbar_wait(&q_full[qb], (qn / QBUF) & 1, abort_flag, p.err))) break;
           tc_fence_after();
           ++qn;
-          return got;
-        };
-        // stage n's K as the first tile of item x
-        auto first_s = [&](const Item& x) -> bool {
-          if (!wait_q()) return false;
-          const int st = n % STAGES, qb = (qn - 1) % QBUF;
+          int st = n % STAGES;
+          if (!(ok = wait_stage(st))) break;
 #pragma unroll
           for (int i = 0; i < NQ; ++i)
-            if (active(x, i, x.lo_all) && !issue_next_s(i, qb, st)) return false;
-          if (x.hi_all - x.lo_all == 1) mma_commit(&q_empty[qb]);
-          return true;
-        };
-        if (have && ok) {
-          ok = first_s(it);
-          mma_commit(&empty[0]);
+            if (ok && active(it, i, it.lo_all)) ok = issue_next_s(i, qb, st);
+          if (!ok) break;
+          mma_commit(&empty[st]);
           ++n;
-        }
-        while (have && ok) {
-          const int qb = (qn - 1) % QBUF;
-          bool more = false;
+          if (it.hi_all - it.lo_all == 1) mma_commit(&q_empty[qb]);
           for (int j = it.lo_all; j < it.hi_all && ok; ++j) {
-            const int st = n % STAGES;
-            if (!(ok = wait_stage(st))) break;
-            bool tail = false;
             if (j + 1 < it.hi_all) {
+              st = n % STAGES;
+              if (!(ok = wait_stage(st))) break;
 #pragma unroll
               for (int i = 0; i < NQ; ++i)
                 if (ok && active(it, i, j + 1)) ok = issue_next_s(i, qb, st);
+              if (!ok) break;
+              mma_commit(&empty[st]);
+              ++n;
               if (j + 1 == it.hi_all - 1) mma_commit(&q_empty[qb]);
-            } else {
-              tail = tail_start(it);
-              more = next_work(r, false, nx);
-              if (more) ok = first_s(nx);
             }
+            st = n % STAGES;
+            if (!(ok = wait_stage(st))) break;
+            bool tail = j + 1 == it.hi_all && tail_start(it);
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
               if (!ok || !active(it, i, j)) continue;
@@ -575,12 +584,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             mma_commit(&empty[st]);
             ++n;
           }
-          it = nx;
-          have = more;
+          if (ok) have = next_work(r, false, it);
         }
       } else {
         // Per key tile j and query tile i: P_i(j) V_j as soon as softmax group i has written P_i(j) over
         // S_i(j), then S_i(j + 1); one group's softmax overlaps the other group's products.
+        if (have) ok = wait_stage(0);
         while (have && ok) {
           const int qb = qn % QBUF;
           if (!(ok = mbar_wait(&q_full[qb], (qn / QBUF) & 1, abort_flag, p.err))) break;
@@ -634,14 +643,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     const int tpt = BM >> p.pack_log2;
     const int tb_log2 = 7 - p.pack_log2 + (p.tiles - 1);
     const int chunks = (p.B + 31) / 32;
-    PackedLevels first = {0, 0};
-    if (lane < p.B) first = packed_levels<PAGED>(p, lane, tb_log2);
-    auto levels_of = [&](int c) -> PackedLevels {   // sequence 32 c + lane
-      if (c == 0) return first;
-      PackedLevels l = {0, 0};
-      if (c * 32 + lane < p.B) l = packed_levels<PAGED>(p, c * 32 + lane, tb_log2);
-      return l;
+    // sequence 32 c + lane; the first 32 stay in registers
+    auto span_of = [&](int c) -> PackedSpan {
+      PackedSpan s = {0, 0, 0, 0};
+      if (c * 32 + lane < p.B) s = packed_span<PAGED>(p, c * 32 + lane);
+      return s;
     };
+    const PackedSpan span0 = span_of(0);
+    auto levels_of = [&](int c) -> PackedLevels { return packed_levels(p, c == 0 ? span0 : span_of(c), tb_log2); };
+    const int blocks_per_kv = p.Hq / p.Hkv >> p.pack_log2;   // head blocks of a kv head
     int level = 0x7FFFFFFF, below = -1, base = 0, count = 0;
     auto visit = [&](int q) {   // blocks at level q, and the next level that has any
       int m = 0, nx = -1;
@@ -683,13 +693,20 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (level >= 0) {
           int j = rank - base;   // the j-th block of this level
           for (int ch = 0; ch < chunks; ++ch) {
-            const PackedLevels l = levels_of(ch);
+            const PackedSpan sp = ch == 0 ? span0 : span_of(ch);
+            const PackedLevels l = packed_levels(p, sp, tb_log2);
             const int m = blocks_at(l, p.causal, level);
-            int incl = m;
+            // inclusive count over the lanes: of ones where a sequence has one block at most
+            const bool ones = p.causal && level > 0;
+            const unsigned int set = __ballot_sync(0xffffffffu, m > 0);
+            int incl = __popc(set & (0xffffffffu >> (31 - lane)));
+            if (!ones) {
+              incl = m;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-              const int v = __shfl_up_sync(0xffffffffu, incl, d);
-              if (lane >= d) incl += v;
+              for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += v;
+              }
             }
             const int total = __shfl_sync(0xffffffffu, incl, 31);
             if (j >= total) {
@@ -699,19 +716,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             const int src = __ffs(__ballot_sync(0xffffffffu, incl > j)) - 1;
             j -= __shfl_sync(0xffffffffu, incl - m, src);
             const int o = __shfl_sync(0xffffffffu, l.o, src), nb = __shfl_sync(0xffffffffu, l.nb, src);
-            const int qb = (p.causal && level > 0) ? level - o : j;
+            const int qb = ones ? level - o : j;
             // (counts of malformed, overlapping lengths may have wrapped: no block then)
             if (src < 0 || ch * 32 + src >= p.B || qb < 0 || qb >= nb) break;
             it.b = ch * 32 + src;
-            const PackedSpan s = packed_span<PAGED>(p, it.b);
             it.hb = k - rank * p.head_blocks;
-            it.g = (it.hb << p.pack_log2) / (p.Hq / p.Hkv);
+            it.g = blocks_per_kv == 1 ? it.hb : it.hb / blocks_per_kv;
             it.row0 = qb << tb_log2;
-            it.end = min(s.sq, it.row0 + p.tiles * tpt);
-            it.q_base = s.q0;
-            it.k_base = s.k0;
-            it.sq = s.sq;
-            it.sk = s.sk;
+            it.q_base = __shfl_sync(0xffffffffu, sp.q0, src);
+            it.k_base = __shfl_sync(0xffffffffu, sp.k0, src);
+            it.sq = __shfl_sync(0xffffffffu, sp.sq, src);
+            it.sk = __shfl_sync(0xffffffffu, sp.sk, src);
+            it.end = min(it.sq, it.row0 + p.tiles * tpt);
             packed_ranges(p, it);
             break;
           }
@@ -736,13 +752,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     }
    } else if (warp == kTailWarp) {
     // ------------------------------------------------------------ V rows behind a sequence
-    int n = 0, tails = 0;   // key tiles of the items so far (stage n holds the V of the last), tiles zeroed
+    int tiles = 0, tails = 0;   // key tiles of the items so far, V tiles zeroed
     for (int r = 0;; ++r) {
       Item it;
       if (!__all_sync(0xffffffffu, mbar_wait_idle(&item_full[r % kItemRing], (r / kItemRing) & 1, abort_flag, p.err)))
         break;
       if (!next_item(r, true, it)) break;
-      n += it.hi_all - it.lo_all;
+      tiles += it.hi_all - it.lo_all;
+      const int n = C::SEP_P ? 2 * tiles - 1 : tiles;   // number of the stage of the item's last V
       int from, to;
       v_tail<PAGED>(p, it, from, to);
       if (to <= from) continue;
