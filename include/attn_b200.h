@@ -108,7 +108,7 @@ typedef enum {
   ATTN_ERR_BAD_PAGE = 5,      /* a page-table entry was outside [0, num_pages), or a sequence was
                                  longer than max_pages * page_size or max_seq_len
                                  (reported by attn_device_status) */
-  ATTN_ERR_WORKSPACE = 6,     /* workspace missing or smaller than attn_decode_paged_workspace_size */
+  ATTN_ERR_WORKSPACE = 6,     /* workspace missing (decode), misaligned, or smaller than the *_workspace_size */
   ATTN_ERR_OUT_OF_PAGES = 7   /* the page pool has too few free pages for a request (nothing changed) */
 } attn_status_t;
 
@@ -269,6 +269,12 @@ attn_status_t attn_prefill_paged(const void* q, const void* k_pool, const void* 
  * lse    : [Tq, Hq] float or NULL (as attn_prefill_lse)
  * D, scale, causal, window : as attn_prefill, per sequence: off is the
  *          sequence's own number of keys minus its number of queries.
+ * workspace : NULL, or device scratch of at least
+ *          attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, ceil(Tk / B))
+ *          bytes, 16-byte aligned.  With it, a call with few query rows over long
+ *          sequences deals each row's keys to several SMs and joins the parts
+ *          (the split depends on the sizes in that call alone).  Contents are not
+ *          needed between calls; two calls in flight at once need two.
  * B at most 65535; Tq and Tk at most 2^30 rows.
  *
  * A sequence may be empty on either side (a query without keys gives 0 and
@@ -281,14 +287,22 @@ attn_status_t attn_prefill_paged(const void* q, const void* k_pool, const void* 
  * 128-key tile that do not see it (0 * NaN).  A cumulative length that
  * decreases, is negative or passes Tq (Tk) is cut to the buffer and reported
  * as ATTN_ERR_BAD_PAGE by attn_device_status.
- * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
+ * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_WORKSPACE (a
+ * workspace that is too small or misaligned), ATTN_ERR_CUDA.
  */
 attn_status_t attn_prefill_packed(const void* q, const void* k, const void* v,
                                   const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
                                   int B, int Tq, int Tk, int Hq, int Hkv, int D,
                                   int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
                                   float scale, int causal, int window,
+                                  void* workspace, size_t workspace_bytes,
                                   void* out, float* lse, attn_stream_t stream);
+
+/* Bytes of workspace with which attn_prefill_packed_paged, and attn_prefill_packed
+ * (max_seq_len: Tk / B rounded up, as if its sequences were equally long), split
+ * long sequences; 0 for sizes that are not split, or invalid.  Pure host
+ * arithmetic, no CUDA call. */
+size_t attn_prefill_packed_workspace_size(int B, int Tq, int Hq, int Hkv, int D, int max_seq_len);
 
 /*
  * attn_prefill_packed_paged -- attn_prefill_packed whose keys and values sit in
@@ -302,9 +316,9 @@ attn_status_t attn_prefill_packed(const void* q, const void* k, const void* v,
  * max_seq_len : as attn_prefill_paged (seq_lens counts the new tokens, already
  *              appended; max_seq_len at most 2^30), with its treatment of
  *              slots behind the last token and of bad pages.
- * For single tokens attn_decode_paged splits a long cache over the GPU; this
- * call gives each (sequence, group of heads) to one SM.
- * Errors: ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA.
+ * workspace  : as attn_prefill_packed, of
+ *              attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len) bytes
+ * Errors: as attn_prefill_packed.
  */
 attn_status_t attn_prefill_packed_paged(const void* q, const void* k_pool, const void* v_pool,
                                         const int32_t* cu_seqlens_q, const int32_t* page_table,
@@ -312,6 +326,7 @@ attn_status_t attn_prefill_packed_paged(const void* q, const void* k_pool, const
                                         int D, int64_t q_stride, int64_t out_stride,
                                         int num_pages, int max_pages, int max_seq_len,
                                         float scale, int causal, int window,
+                                        void* workspace, size_t workspace_bytes,
                                         void* out, float* lse, attn_stream_t stream);
 
 /*

@@ -34,9 +34,11 @@ PROTOTYPES = {
     "attn_selftest_wait_timeout": (_c_int, [_c_int, _vp]),
     "attn_kv_append": (_c_int, [_vp] * 6 + [_c_int] * 7 + [_vp]),
     "attn_kv_append_fp8": (_c_int, [_vp] * 6 + [_c_int] * 7 + [_c_float, _c_float, _vp]),
-    "attn_prefill_packed": (_c_int, [_vp] * 5 + [_c_int] * 6 + [_c_i64] * 4 + [_c_float, _c_int, _c_int, _vp, _vp, _vp]),
+    "attn_prefill_packed": (_c_int, [_vp] * 5 + [_c_int] * 6 + [_c_i64] * 4
+                            + [_c_float, _c_int, _c_int, _vp, _c_size, _vp, _vp, _vp]),
+    "attn_prefill_packed_workspace_size": (_c_size, [_c_int] * 6),
     "attn_prefill_packed_paged": (_c_int, [_vp] * 6 + [_c_int] * 6 + [_c_i64] * 2 + [_c_int] * 3
-                                  + [_c_float, _c_int, _c_int, _vp, _vp, _vp]),
+                                  + [_c_float, _c_int, _c_int, _vp, _c_size, _vp, _vp, _vp]),
     "attn_kv_append_rope": (_c_int, [_vp] * 11 + [_c_int] * 8 + [_c_i64] * 5 + [_c_int] * 3 + [_vp]),
     "attn_kv_append_rope_fp8": (_c_int, [_vp] * 11 + [_c_int] * 8 + [_c_i64] * 5 + [_c_int] * 3
                                 + [_c_float, _c_float, _vp]),

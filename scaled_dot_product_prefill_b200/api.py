@@ -17,7 +17,8 @@ __all__ = ["attn_prefill", "attn_prefill_f32", "attn_prefill_lse", "attn_prefill
            "attn_prefill_paged", "attn_prefill_host", "attn_decode_paged", "attn_decode_paged_noalloc",
            "attn_decode_step_host",
            "attn_decode_paged_workspace_size", "attn_decode_paged_fp8", "attn_kv_append", "attn_kv_append_fp8",
-           "attn_prefill_packed", "attn_prefill_packed_paged", "attn_kv_append_rope", "attn_kv_append_rope_fp8",
+           "attn_prefill_packed", "attn_prefill_packed_paged", "attn_prefill_packed_workspace_size",
+           "attn_kv_append_rope", "attn_kv_append_rope_fp8",
            "PagePool",
            "attn_device_status", "attn_selftest_wait_timeout", "attn_status_string", "attn_version", "AttnError"]
 
@@ -527,15 +528,35 @@ def _packed_results(q, Tq, Hq, D, out, lse, want_lse):
             None if lse is None else _shaped(lse, "lse", (Tq, Hq), torch.float32), made)
 
 
+def attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len) -> int:
+    return int(_lib.load().attn_prefill_packed_workspace_size(int(B), int(Tq), int(Hq), int(Hkv), int(D),
+                                                              int(max_seq_len)))
+
+
+def _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, max_seq_len, device):
+    """The workspace, its pointer and its size in bytes, and what was allocated here (sizes that never split need none)."""
+    if workspace is None:
+        need = _lib.load().attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len)
+        if need == 0:
+            return None, None, 0, made
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        made += (workspace,)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size(), made
+
+
 def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True, window=0, scale=None, out=None,
-                        lse=None, want_lse=False, stream=None):
+                        lse=None, want_lse=False, workspace=None, stream=None):
     """bf16 prefill of sequences of different lengths, packed: q [Tq,Hq,D], k/v [Tk,Hkv,D] -> out [Tq,Hq,D].
 
     Sequence b holds rows cu_seqlens_q[b]:cu_seqlens_q[b+1] of q and out, and
     cu_seqlens_k[b]:cu_seqlens_k[b+1] of k and v (default: the same).  The cumulative
     lengths are int32 [B+1] CUDA tensors.  q, k, v and out may have any token stride that is
     a multiple of 8 (slices of a fused projection).  Rows that no sequence holds are left
-    as they were.  Returns out, or (out, lse) with want_lse (or an lse tensor given); lse [Tq,Hq] fp32.
+    as they were.  `workspace`: device scratch of attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D,
+    ceil(Tk / B)) bytes, allocated here if None.  Returns out, or (out, lse) with want_lse (or an lse tensor given);
+    lse [Tq,Hq] fp32.
     """
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [tokens, heads, D]")
@@ -552,22 +573,25 @@ def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True
     cu_q = _shaped(cu_seqlens_q, "cu_seqlens_q", (B + 1,), torch.int32)
     cu_k = _shaped(cu_seqlens_k, "cu_seqlens_k", (B + 1,), torch.int32)
     out, out_stride, lse, lse_ptr, made = _packed_results(q, Tq, Hq, D, out, lse, want_lse)
-    dev = _on_device((q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse),
-                     ("q", "k", "v", "cu_seqlens_q", "cu_seqlens_k", "out", "lse"))
+    workspace, ws_ptr, ws_bytes, made = _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, -(-Tk // max(B, 1)),
+                                                          q.device)
+    dev = _on_device((q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace),
+                     ("q", "k", "v", "cu_seqlens_q", "cu_seqlens_k", "out", "lse", "workspace"))
     _check("attn_prefill_packed", _lib.load().attn_prefill_packed(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
         out_stride, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)), int(window),
-        out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
+        ws_ptr, ws_bytes, out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
     return out if lse is None else (out, lse)
 
 
 def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, *, max_seq_len, causal=True,
-                              window=0, scale=None, out=None, lse=None, want_lse=False, stream=None):
+                              window=0, scale=None, out=None, lse=None, want_lse=False, workspace=None, stream=None):
     """Chunked prefill of packed queries over the paged cache: q [Tq,Hq,D], each sequence its own number of rows.
 
     Rows cu_seqlens_q[b]:cu_seqlens_q[b+1] are the newest tokens of sequence b, whose cache (pools
     [num_pages,Hkv,page_size,D], page_table [B,max_pages], seq_lens [B]) already holds them.
-    Strides, rows of no sequence and the result are as attn_prefill_packed's.
+    Strides, rows of no sequence, the workspace (here for max_seq_len) and the result are as
+    attn_prefill_packed's.
     """
     if q.dim() != 3 or k_pool.dim() != 4 or page_table.dim() != 2:
         raise ValueError("q must be [tokens,Hq,D], the pools [num_pages,Hkv,page_size,D], page_table [B,max_pages]")
@@ -583,12 +607,14 @@ def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_l
     table = _shaped(page_table, "page_table", (B, max_pages), torch.int32)
     lens = _shaped(seq_lens, "seq_lens", (B,), torch.int32)
     out, out_stride, lse, lse_ptr, made = _packed_results(q, Tq, Hq, D, out, lse, want_lse)
-    dev = _on_device((q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, out, lse),
-                     ("q", "k_pool", "v_pool", "cu_seqlens_q", "page_table", "seq_lens", "out", "lse"))
+    max_seq_len = int(max_seq_len)
+    workspace, ws_ptr, ws_bytes, made = _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, max_seq_len, q.device)
+    dev = _on_device((q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, out, lse, workspace),
+                     ("q", "k_pool", "v_pool", "cu_seqlens_q", "page_table", "seq_lens", "out", "lse", "workspace"))
     _check("attn_prefill_packed_paged", _lib.load().attn_prefill_packed_paged(
         q.data_ptr(), kp, vp, cu_q, table, lens, page_size, B, Tq, Hq, Hkv, D, q_stride, out_stride, num_pages,
-        max_pages, int(max_seq_len), 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)),
-        int(window), out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
+        max_pages, max_seq_len, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)),
+        int(window), ws_ptr, ws_bytes, out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
     return out if lse is None else (out, lse)
 
 

@@ -214,15 +214,26 @@ attn_status_t from_packed(cudaError_t e) {
   return from_cuda(e);
 }
 
+// No workspace, or one that holds what the call would put there.
+bool good_workspace(const void* workspace, size_t bytes, size_t need) {
+  return workspace == nullptr || (bytes >= need && aligned16(workspace));
+}
+
 // A window this long hides nothing that int32 positions can hold.
 int cut_window(int window) { return window < (1 << 30) ? window : (1 << 30); }
 
 }  // namespace
 
+size_t attn_prefill_packed_workspace_size(int B, int Tq, int Hq, int Hkv, int D, int max_seq_len) {
+  if (B <= 0 || Tq <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_seq_len < 0) return 0;
+  return attn::packed_workspace_bytes(B, Tq, Hq, Hkv, D, max_seq_len);
+}
+
 attn_status_t attn_prefill_packed(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
                                   const int32_t* cu_seqlens_k, int B, int Tq, int Tk, int Hq, int Hkv, int D,
                                   int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
-                                  float scale, int causal, int window, void* out, float* lse, attn_stream_t stream) {
+                                  float scale, int causal, int window, void* workspace, size_t workspace_bytes,
+                                  void* out, float* lse, attn_stream_t stream) {
   const attn_status_t st =
       check_packed(q, cu_seqlens_q, out, lse, B, Tq, Hq, Hkv, D, q_stride, out_stride, scale, causal, window);
   if (st != ATTN_OK || B == 0 || Tq == 0 || Hq == 0) return Tk < 0 ? ATTN_ERR_INVALID_ARG : st;
@@ -232,9 +243,11 @@ attn_status_t attn_prefill_packed(const void* q, const void* k, const void* v, c
   if (!aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID_ARG;
   if (!good_stride(k_stride, Hkv, D) || !good_stride(v_stride, Hkv, D)) return ATTN_ERR_INVALID_ARG;
   if (Tk > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  if (!good_workspace(workspace, workspace_bytes, attn::packed_workspace_bytes(B, Tq, Hq, Hkv, D, attn::keys_each(Tk, B))))
+    return ATTN_ERR_WORKSPACE;
   return from_packed(attn::launch_prefill_tc_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, B, Tq, Tk, Hq, Hkv, D,
                                                     q_stride, k_stride, v_stride, out_stride, scale, causal,
-                                                    cut_window(window), out, lse, attn::device_error_word(),
+                                                    cut_window(window), workspace, out, lse, attn::device_error_word(),
                                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -242,8 +255,8 @@ attn_status_t attn_prefill_packed_paged(const void* q, const void* k_pool, const
                                         const int32_t* cu_seqlens_q, const int32_t* page_table,
                                         const int32_t* seq_lens, int page_size, int B, int Tq, int Hq, int Hkv, int D,
                                         int64_t q_stride, int64_t out_stride, int num_pages, int max_pages,
-                                        int max_seq_len, float scale, int causal, int window, void* out, float* lse,
-                                        attn_stream_t stream) {
+                                        int max_seq_len, float scale, int causal, int window, void* workspace,
+                                        size_t workspace_bytes, void* out, float* lse, attn_stream_t stream) {
   const attn_status_t st =
       check_packed(q, cu_seqlens_q, out, lse, B, Tq, Hq, Hkv, D, q_stride, out_stride, scale, causal, window);
   if (num_pages < 0 || max_pages < 0 || max_seq_len < 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
@@ -259,9 +272,12 @@ attn_status_t attn_prefill_packed_paged(const void* q, const void* k_pool, const
   if (max_seq_len > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
   // TMA plane coordinates (page * Hkv + g, one page past the pool for boxes past a sequence end) are int32
   if ((static_cast<long long>(num_pages) + 1) * Hkv > 0x7FFFFFFFLL) return ATTN_ERR_UNSUPPORTED;
+  if (!good_workspace(workspace, workspace_bytes, attn::packed_workspace_bytes(B, Tq, Hq, Hkv, D, max_seq_len)))
+    return ATTN_ERR_WORKSPACE;
   return from_packed(attn::launch_prefill_tc_packed_paged(
       q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, page_size, B, Tq, Hq, Hkv, D, q_stride, out_stride,
-      num_pages, max_pages, max_seq_len, scale, causal, cut_window(window), out, lse, attn::device_error_word(),
+      num_pages, max_pages, max_seq_len, scale, causal, cut_window(window), workspace, out, lse,
+      attn::device_error_word(),
       reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -81,17 +81,22 @@ cudaError_t launch_prefill_tc_paged(const void* q, const void* k_pool, const voi
                                     int num_pages, int max_pages, int max_seq_len, float scale, int causal,
                                     int window, void* out, float* lse, unsigned int* err, cudaStream_t stream);
 // Packed sequences: q/out [Tq, Hq, D], k/v [Tk, Hkv, D] with token strides in elements, cumulative
-// lengths cu_q, cu_k [B + 1] on the device; lse (optional) [Tq, Hq].
+// lengths cu_q, cu_k [B + 1] on the device; lse (optional) [Tq, Hq].  The workspace (optional, of
+// packed_workspace_bytes) lets the key tiles of few items be dealt to packed_splits parts each.
+int packed_splits(int B, int Tq, int Hq, int Hkv, int max_seq_len);
+inline int keys_each(int Tk, int B) { return B > 0 ? static_cast<int>((static_cast<long long>(Tk) + B - 1) / B) : 0; }
+size_t packed_workspace_bytes(int B, int Tq, int Hq, int Hkv, int D, int max_seq_len);
 cudaError_t launch_prefill_tc_packed(const void* q, const void* k, const void* v, const int32_t* cu_q,
                                      const int32_t* cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int D,
                                      long long q_stride, long long k_stride, long long v_stride, long long out_stride,
-                                     float scale, int causal, int window, void* out, float* lse, unsigned int* err,
-                                     cudaStream_t stream);
+                                     float scale, int causal, int window, void* workspace, void* out, float* lse,
+                                     unsigned int* err, cudaStream_t stream);
 cudaError_t launch_prefill_tc_packed_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* cu_q,
                                            const int32_t* page_table, const int32_t* seq_lens, int page_size, int B,
                                            int Tq, int Hq, int Hkv, int D, long long q_stride, long long out_stride,
                                            int num_pages, int max_pages, int max_seq_len, float scale, int causal,
-                                           int window, void* out, float* lse, unsigned int* err, cudaStream_t stream);
+                                           int window, void* workspace, void* out, float* lse, unsigned int* err,
+                                           cudaStream_t stream);
 cudaError_t launch_prefill_f32(const float* q, const float* k, const float* v, float* out, float* lse, int B,
                                int Hq, int Hkv, int Sq, int Skv, int D, float scale, int causal, int window,
                                cudaStream_t stream);

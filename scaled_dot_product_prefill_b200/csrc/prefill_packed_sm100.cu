@@ -41,6 +41,12 @@
 // row's 128 bytes together: one thread a row would touch 32 lines with every
 // store (4 % of the time of a batch of 1 to 1024-token prompts).
 //
+// Split.  With so few items that each could have several SMs (a few new tokens
+// of a few sequences), the key tiles of an item are dealt to 2 to 16 items
+// (SPLIT kernels; packed_splits has the rule and what it measured).  Each writes its
+// normalised fp32 output rows and base-2 log-sum-exps to the caller's workspace,
+// and prefill_packed_combine_kernel joins them.
+//
 // Tensor memory (512 columns x 128 lanes, fp32), as in the dense kernel:
 //   D = 128: S_i at 128 i, P_i (bf16) over its first half, O_i at 256 + 128 i
 //   D = 64:  S_i at 128 i, P_i at 256 + 64 i, O_i at 384 + 64 i; S_i(j + 1)
@@ -107,10 +113,14 @@ struct Params {
   const int32_t* page_table;
   const int32_t* seq_lens;
   int page_size, box_rows, max_pages, num_pages, max_seq_len;
+  // SPLIT: the items an item's key tiles are dealt to, and their results
+  int splits;
+  float* ws_o;              // [splits, Tq, Hq, D]
+  float* ws_lse;            // [splits, Tq, Hq], log2 units
 };
 
 struct Item {
-  int b;                // sequence; -1 ends the list
+  int b;                // sequence (SPLIT: in the low 16 bits, above them the part); -1 ends the list
   int hb, g;            // head block (heads [hb << s, (hb + 1) << s)) and its kv head
   int row0, end;        // tokens [row0, end) of the sequence
   int q_base, k_base;   // the sequence's first rows
@@ -210,6 +220,26 @@ __device__ __forceinline__ void packed_ranges(const Params& p, Item& it) {
   if (it.hi_all <= 0) it.lo_all = it.hi_all = 0;
 }
 
+// SPLIT: the item's ranges cut to share `part` of its key tiles.
+__device__ __forceinline__ void cut_to_part(const Params& p, Item& it, int part) {
+  const int n = it.hi_all - it.lo_all;
+  const int from = it.lo_all + n * part / p.splits, to = it.lo_all + n * (part + 1) / p.splits;
+  it.lo_all = 1 << 30;
+  it.hi_all = 0;
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    it.lo[i] = max(it.lo[i], from);
+    it.hi[i] = min(it.hi[i], to);
+    if (it.hi[i] > it.lo[i]) {
+      it.lo_all = min(it.lo_all, it.lo[i]);
+      it.hi_all = max(it.hi_all, it.hi[i]);
+    } else {
+      it.lo[i] = it.hi[i] = 0;
+    }
+  }
+  if (it.hi_all <= 0) it.lo_all = it.hi_all = 0;
+}
+
 // Rows [from, to) of the item's last V tile lie behind its sequence and must be
 // zeroed before P V reads them (to <= from: none).  Packed rows behind a
 // sequence are the next one's; of paged ones only the box that holds the last
@@ -234,7 +264,7 @@ __device__ __forceinline__ bool tile_unmasked(const Params& p, const Item& it, i
   return true;
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool SPLIT>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     prefill_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_v, const Params p) {
@@ -376,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           if (lane < nb * C::KATOMS) {
             const int key0 = j * BN + (lane % nb) * p.box_rows;
             if (key0 < it.sk) {
-              ph = p.page_table[static_cast<size_t>(it.b) * p.max_pages + key0 / p.page_size];
+              ph = p.page_table[static_cast<size_t>(SPLIT ? it.b & 0xFFFF : it.b) * p.max_pages + key0 / p.page_size];
               if (ph < 0 || ph >= p.num_pages) {  // never read outside the pool
                 record_error(p.err, ATTN_ERRBIT_BADPAGE);
                 ph = 0;
@@ -677,7 +707,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       for (int r = 0;; ++r) {
         const int P = gridDim.x, c = blockIdx.x;
         const int k = r * P + ((r & 1) ? (P - 1 - c) : c);
-        const int rank = k / p.head_blocks;
+        const int unit = SPLIT ? k / p.splits : k;
+        const int rank = unit / p.head_blocks;
         while (level >= 0 && rank >= base + count) {
           base += count;
           if (below < 0) level = -1;
@@ -720,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             // (counts of malformed, overlapping lengths may have wrapped: no block then)
             if (src < 0 || ch * 32 + src >= p.B || qb < 0 || qb >= nb) break;
             it.b = ch * 32 + src;
-            it.hb = k - rank * p.head_blocks;
+            it.hb = unit - rank * p.head_blocks;
             it.g = blocks_per_kv == 1 ? it.hb : it.hb / blocks_per_kv;
             it.row0 = qb << tb_log2;
             it.q_base = __shfl_sync(0xffffffffu, sp.q0, src);
@@ -729,6 +760,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             it.sk = __shfl_sync(0xffffffffu, sp.sk, src);
             it.end = min(it.sq, it.row0 + p.tiles * tpt);
             packed_ranges(p, it);
+            if constexpr (SPLIT) {
+              cut_to_part(p, it, k - unit * p.splits);
+              it.b |= (k - unit * p.splits) << 16;
+            }
             break;
           }
         }
@@ -824,8 +859,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const bool store = r < it.end;
       auto head = [&]() -> int { return (it.hb << p.pack_log2) + (rl & ((1 << p.pack_log2) - 1)); };
       auto lse_at = [&]() -> size_t { return (static_cast<size_t>(it.q_base) + r) * p.Hq + head(); };
+      auto ws_at = [&]() -> size_t { return static_cast<size_t>(it.b >> 16) * p.Tq * p.Hq + lse_at(); };   // SPLIT
       if (my_hi <= my_lo) {                  // no visible key for any row of this tile
-        if (store) {
+        if (SPLIT && store) {
+          p.ws_lse[ws_at()] = -INFINITY;
+        } else if (store) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(it.q_base) + r) * p.out_stride +
                                                 static_cast<size_t>(head()) * D);
           for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -934,41 +972,58 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // a row with no visible key is 0 (and its lse -inf)
       const bool has_keys = key_hi >= max(key_lo, 0);
       const float inv = (has_keys && l > 0.f) ? 1.f / l : 0.f;
-      if (p.lse != nullptr && store)   // log(sum_j exp(s_ij * scale)) = (m + log2 l) * ln 2
-        p.lse[lse_at()] =
-            (has_keys && l > 0.f) ? (m_ref + log2f(l)) * 0.6931471805599453f : -INFINITY;
-      // (64 columns of the warp's 32 rows at a time; the 16-byte pieces of a row are permuted by its
-      // number, which keeps both sides free of bank conflicts)
-      uint8_t* stage = sOut + warp * 4096;
+      if constexpr (SPLIT) {
+        const size_t at = ws_at();
+        if (store) p.ws_lse[at] = l == 0.f ? -INFINITY : m_ref + log2f(l);   // (NaN stays NaN)
 #pragma unroll 1
-      for (int h = 0; h < D / 64; ++h) {
-        __syncwarp();   // the warp has read the half before
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
-          tmem_ld32(o_tmem + 64 * h + 32 * c, o);
+          tmem_ld32(o_tmem + 32 * c, o);
           tmem_wait_ld();
+          if (store) {
+            float4* dst = reinterpret_cast<float4*>(p.ws_o + at * D + 32 * c);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
-            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + e) ^ (lane & 7)) * 16)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                   __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
           }
         }
-        __syncwarp();
+      } else {
+        if (p.lse != nullptr && store)   // log(sum_j exp(s_ij * scale)) = (m + log2 l) * ln 2
+          p.lse[lse_at()] = (!has_keys || l == 0.f) ? -INFINITY : (m_ref + log2f(l)) * 0.6931471805599453f;
+        // (64 columns of the warp's 32 rows at a time; the 16-byte pieces of a row are permuted by its
+        // number, which keeps both sides free of bank conflicts)
+        uint8_t* stage = sOut + warp * 4096;
+#pragma unroll 1
+        for (int h = 0; h < D / 64; ++h) {
+          __syncwarp();   // the warp has read the half before
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int row = 4 * e + (lane >> 3), piece = lane & 7;
-          const uint4 u = *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) * 16));
-          const int at = wq * 32 + row;                      // row within the tile
-          const int tok = r0 + (at >> p.pack_log2);
-          const int hd = (it.hb << p.pack_log2) + (at & ((1 << p.pack_log2) - 1));
-          if (tok < it.end)
-            *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(it.q_base) + tok) * p.out_stride +
-                                      static_cast<size_t>(hd) * D + 64 * h + piece * 8) = u;
+          for (int c = 0; c < 2; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_tmem + 64 * h + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + e) ^ (lane & 7)) * 16)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int row = 4 * e + (lane >> 3), piece = lane & 7;
+            const uint4 u = *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) * 16));
+            const int at = wq * 32 + row;                      // row within the tile
+            const int tok = r0 + (at >> p.pack_log2);
+            const int hd = (it.hb << p.pack_log2) + (at & ((1 << p.pack_log2) - 1));
+            if (tok < it.end)
+              *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(it.q_base) + tok) * p.out_stride +
+                                        static_cast<size_t>(hd) * D + 64 * h + piece * 8) = u;
+          }
         }
       }
       tc_fence_before();   // this group's O reads precede the next item's first P_i V product
@@ -1008,7 +1063,7 @@ bool make_map_packed_kv(CUtensorMap* m, const void* base, int D, int tokens, int
 
 // One-time set-up of a kernel on the current device: its shared-memory limit, and the check
 // that setmaxnreg.inc can be honoured (as the dense kernel's).
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool SPLIT>
 cudaError_t prepare_kernel() {
   using C = Cfg<D>;
   constexpr int kMaxDevices = 64;
@@ -1016,7 +1071,7 @@ cudaError_t prepare_kernel() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (__atomic_load_n(&ready[dev], __ATOMIC_ACQUIRE) == 1) return cudaSuccess;
-  auto kern = prefill_packed_kernel<D, PAGED>;
+  auto kern = prefill_packed_kernel<D, PAGED, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::SMEM));
   if (e != cudaSuccess) return e;
   cudaFuncAttributes fa{};
@@ -1028,12 +1083,12 @@ cudaError_t prepare_kernel() {
   return cudaSuccess;
 }
 
-template <int D, bool PAGED>
-cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p,
+template <int D, bool PAGED, bool SPLIT>
+cudaError_t launch_s(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p,
                      cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kern = prefill_packed_kernel<D, PAGED>;
-  cudaError_t e = prepare_kernel<D, PAGED>();
+  auto kern = prefill_packed_kernel<D, PAGED, SPLIT>;
+  cudaError_t e = prepare_kernel<D, PAGED, SPLIT>();
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
@@ -1041,10 +1096,106 @@ cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   return launch_dependent(kern, dim3(grid), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p);
 }
 
-// What the packed launches share: the head packing, the item bound that sizes the
-// grid, and the fields of Params that do not depend on where K and V lie.
-bool packed_params(Params& p, const void* out, float* lse, const int32_t* cu_q, int B, int Hq, int Hkv, int Tq,
-                   long long out_stride, float scale, int causal, int window, unsigned int* err) {
+// Joins the parts of each row of a sequence: a warp a row, its lanes over the columns.
+template <int D>
+__global__ void __launch_bounds__(128) prefill_packed_combine_kernel(const Params p) {
+  constexpr int PER = D / 32;
+  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  grid_dependency_wait();   // the parts
+  const int t = static_cast<int>(row / p.Hq);
+  if (t >= p.Tq || t < p.cu_q[0] || t >= p.cu_q[p.B]) return;   // rows of no sequence stay as they are
+  const long long rows = static_cast<long long>(p.Tq) * p.Hq;
+  const float lse = lane < p.splits ? p.ws_lse[lane * rows + row] : -INFINITY;   // at most 16 parts
+  float M = lse;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float w = (lse == -INFINITY) ? 0.f : ex2(lse - M);
+  float sum = w;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  float acc[PER];
+#pragma unroll
+  for (int c = 0; c < PER; ++c) acc[c] = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const float ws = __shfl_sync(0xffffffffu, w, s);
+    if (ws == 0.f) continue;   // (a part without keys wrote no row)
+    const float* src = p.ws_o + (s * rows + row) * D + lane * PER;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) acc[c] = fmaf(ws, src[c], acc[c]);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int h = static_cast<int>(row - static_cast<long long>(t) * p.Hq);
+  __nv_bfloat16* dst = p.out + t * p.out_stride + static_cast<long long>(h) * D + lane * PER;
+#pragma unroll
+  for (int c = 0; c < PER; c += 2)
+    *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int D, bool PAGED>
+cudaError_t launch_d(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Params& p,
+                     cudaStream_t stream) {
+  if (p.splits <= 1) return launch_s<D, PAGED, false>(mq, mk, mv, p, stream);
+  const cudaError_t e = launch_s<D, PAGED, true>(mq, mk, mv, p, stream);
+  if (e != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(p.Tq) * p.Hq;   // few: a split has at most 148 items of 256 rows
+  return launch_dependent(prefill_packed_combine_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0,
+                          stream, p);
+}
+
+// 2^s query heads of a kv head share a tile: the largest power of two that divides the group, at most 128.
+int pack_log2_of(int Hq, int Hkv) {
+  int s = 0;
+  while (s < 7 && ((Hq / Hkv) & (1 << s)) == 0) ++s;
+  return s;
+}
+
+// Sequences of any lengths make at most Tq / block + B query blocks; times the head blocks.
+long long item_bound(int B, int Tq, int Hq, int Hkv) {
+  const int s = pack_log2_of(Hq, Hkv);
+  const int block = (BM >> s) * NQ;
+  return (static_cast<long long>(Tq) / block + B) * (Hq >> s);
+}
+
+}  // namespace
+
+// The items that the key tiles of an item are dealt to, from the sizes alone (sequences taken as
+// equally long).  All parts run at once (148 SMs): 8 sequences x 16 new tokens over 8192 keys, 32/8
+// heads, took 153 us whole, 86 in 2 parts (128 items) and 114 in 3; 4 such sequences 151, 86, 64
+// and 50 us in 1 to 4 parts; 2 sequences x 9 tokens, 8/2 heads, 145 us whole and 22 in 16.  With
+// the tiles mostly empty (few rows) a part may be a single key tile: 600 keys took 15.9 us whole
+// and 12.3 in 5.  With full tiles the parts' rows cost as much to write and join as 4 key
+// tiles: a 512-token prompt, 12 heads, took 13.5 us whole and 17.2 in 2, 1024 tokens 20.6 and 19.4.
+int packed_splits(int B, int Tq, int Hq, int Hkv, int max_seq_len) {
+  if (B <= 0 || Tq <= 0 || Hq <= 0 || Hkv <= 0) return 1;
+  const int s = pack_log2_of(Hq, Hkv);
+  const int block = (BM >> s) * NQ;
+  const long long each = (static_cast<long long>(Tq) + B - 1) / B;
+  const long long items = (each + block - 1) / block * B * (Hq >> s);
+  const int tiles = (max_seq_len + BN - 1) / BN;
+  if (tiles < 4) return 1;
+  const bool few_rows = static_cast<long long>(Tq) * Hq <= items * (NQ * BM / 4);
+  long long parts = 148 / items;
+  const int most = few_rows ? tiles : tiles / 4;
+  if (parts > most) parts = most;
+  if (parts > 16) parts = 16;
+  return parts < 2 ? 1 : static_cast<int>(parts);
+}
+
+size_t packed_workspace_bytes(int B, int Tq, int Hq, int Hkv, int D, int max_seq_len) {
+  const int s = packed_splits(B, Tq, Hq, Hkv, max_seq_len);
+  return s < 2 ? 0 : static_cast<size_t>(s) * Tq * Hq * (D + 1) * sizeof(float);
+}
+
+namespace {
+
+// What the packed launches share: the head packing, the item bound that sizes the grid, the
+// split, and the fields of Params that do not depend on where K and V lie.
+bool packed_params(Params& p, void* out, float* lse, const int32_t* cu_q, int B, int Hq, int Hkv, int D, int Tq,
+                   int max_seq_len, long long out_stride, float scale, int causal, int window, void* workspace,
+                   unsigned int* err) {
   p.B = B;
   p.Hq = Hq;
   p.Hkv = Hkv;
@@ -1052,20 +1203,20 @@ bool packed_params(Params& p, const void* out, float* lse, const int32_t* cu_q, 
   p.causal = causal;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out));
+  p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.err = err;
   p.cu_q = cu_q;
   p.out_stride = out_stride;
-  int s = 0;
-  while (s < 7 && ((Hq / Hkv) & (1 << s)) == 0) ++s;   // 2^s divides the group, at most 128 heads
-  p.pack_log2 = s;
-  p.head_blocks = Hq >> s;
-  p.tiles = 2;
-  // sequences of any lengths make at most Tq / block + B blocks; items are counted in int32,
-  // with room for one more round of the grid
-  const int block = (BM >> s) * p.tiles;
-  const long long items = (static_cast<long long>(Tq) / block + B) * p.head_blocks;
+  p.pack_log2 = pack_log2_of(Hq, Hkv);
+  p.head_blocks = Hq >> p.pack_log2;
+  p.tiles = NQ;
+  // the caller's workspace decides whether an item is split (none: never)
+  p.splits = workspace != nullptr ? packed_splits(B, Tq, Hq, Hkv, max_seq_len) : 1;
+  p.ws_o = static_cast<float*>(workspace);
+  if (p.splits > 1) p.ws_lse = p.ws_o + static_cast<size_t>(p.splits) * Tq * Hq * D;
+  // items are counted in int32, with room for one more round of the grid
+  const long long items = item_bound(B, Tq, Hq, Hkv) * p.splits;
   if (items > (1LL << 30)) return false;
   p.n_items = static_cast<int>(items);
   return true;
@@ -1076,10 +1227,11 @@ bool packed_params(Params& p, const void* out, float* lse, const int32_t* cu_q, 
 cudaError_t launch_prefill_tc_packed(const void* q, const void* k, const void* v, const int32_t* cu_q,
                                      const int32_t* cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int D,
                                      long long q_stride, long long k_stride, long long v_stride, long long out_stride,
-                                     float scale, int causal, int window, void* out, float* lse, unsigned int* err,
-                                     cudaStream_t stream) {
+                                     float scale, int causal, int window, void* workspace, void* out, float* lse,
+                                     unsigned int* err, cudaStream_t stream) {
   Params p{};
-  if (!packed_params(p, out, lse, cu_q, B, Hq, Hkv, Tq, out_stride, scale, causal, window, err))
+  if (!packed_params(p, out, lse, cu_q, B, Hq, Hkv, D, Tq, keys_each(Tk, B), out_stride, scale, causal, window, workspace,
+                     err))
     return cudaErrorNotSupported;
   p.cu_k = cu_k;
   p.Tk = Tk;
@@ -1098,9 +1250,11 @@ cudaError_t launch_prefill_tc_packed_paged(const void* q, const void* k_pool, co
                                            const int32_t* page_table, const int32_t* seq_lens, int page_size, int B,
                                            int Tq, int Hq, int Hkv, int D, long long q_stride, long long out_stride,
                                            int num_pages, int max_pages, int max_seq_len, float scale, int causal,
-                                           int window, void* out, float* lse, unsigned int* err, cudaStream_t stream) {
+                                           int window, void* workspace, void* out, float* lse, unsigned int* err,
+                                           cudaStream_t stream) {
   Params p{};
-  if (!packed_params(p, out, lse, cu_q, B, Hq, Hkv, Tq, out_stride, scale, causal, window, err))
+  if (!packed_params(p, out, lse, cu_q, B, Hq, Hkv, D, Tq, max_seq_len, out_stride, scale, causal, window, workspace,
+                     err))
     return cudaErrorNotSupported;
   p.max_seq_len = max_seq_len;
   p.page_table = page_table;

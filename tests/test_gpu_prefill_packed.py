@@ -338,3 +338,115 @@ def test_a_call_on_another_stream_with_its_own_result():
     out = api.attn_prefill_packed(q, k, v, cu, stream=s)
     s.synchronize()
     assert torch.equal(out, want)
+
+
+SPLIT = [
+    # Hq, Hkv, D, page (0: packed keys), query lengths, key lengths, causal, window
+    (8, 2, 128, 16, [5, 1], [3000, 1100], True, 0),
+    (8, 2, 64, 0, [9, 3, 0], [2500, 4, 700], True, 0),          # parts without keys; a sequence without queries
+    (4, 1, 128, 0, [40, 200], [2048, 30], True, 0),             # rows that see nothing
+    (16, 16, 64, 32, [1], [4097], True, 0),
+    (8, 1, 128, 64, [33, 2], [2000, 1500], True, 600),          # most parts lie before the window
+    (4, 4, 128, 256, [3, 17], [1500, 2600], False, 0),
+    (6, 2, 64, 128, [20], [1025], True, 0),
+    (2, 1, 128, 0, [130, 1], [5000, 0], True, 0),
+]
+
+
+@pytest.mark.parametrize("case", SPLIT, ids=[str(c) for c in SPLIT])
+def test_few_rows_over_long_sequences_are_split_and_joined(case):
+    Hq, Hkv, D, page, lq, lk, causal, window = case
+    Tq, cu_q, cu_k = sum(lq) + 3, cumulative(lq, 1), cumulative(lk)
+    q = inputs.normal((Tq, Hq, D), 5)
+    out = torch.full((Tq, Hq, D), 3.5, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((Tq, Hq), -7.25, device="cuda")
+    bound = max(lk) if page else -(-sum(lk) // len(lk))
+    need = api.attn_prefill_packed_workspace_size(len(lq), Tq, Hq, Hkv, D, bound)
+    assert need > 0
+    # a workspace that has been used before: full of NaN
+    ws = torch.full((need // 4,), float("nan"), device="cuda").view(torch.uint8)
+    api.attn_device_status(clear=True)
+    if page:
+        p = inputs.paged_inputs(len(lk), Hq, Hkv, D, page, seed=9, seq_lens=lk, spare_pages=3, poison=True)
+        K, V = gathered(p, lk)
+        call = lambda **kw: api.attn_prefill_packed_paged(  # noqa: E731
+            q.cuda(), p.k_pool.cuda(), p.v_pool.cuda(), cu_q.cuda(), p.page_table.cuda(), p.seq_lens.cuda(),
+            max_seq_len=max(lk), causal=causal, window=window, **kw)
+    else:
+        k, v = inputs.normal((sum(lk), Hkv, D), 6), inputs.normal((sum(lk), Hkv, D), 7)
+        K, V = f64(k), f64(v)
+        call = lambda **kw: api.attn_prefill_packed(  # noqa: E731
+            q.cuda(), k.cuda(), v.cuda(), cu_q.cuda(), cu_k.cuda(), causal=causal, window=window, **kw)
+    call(out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 0
+    assert_packed((out, lse), packed_attention(f64(q), K, V, cu_q.tolist(), cu_k.tolist(), D ** -0.5, causal, window),
+                  str(case))
+    for edge in (slice(0, 1), slice(Tq - 2, Tq)):
+        assert (out[edge] == 3.5).all() and (lse[edge] == -7.25).all()
+    # the same bits from a workspace made in the call
+    again, again_lse = call(want_lse=True)
+    held = slice(1, Tq - 2)
+    assert torch.equal(again[held], out[held]) and torch.equal(again_lse[held], lse[held])
+
+
+def test_a_split_row_whose_scores_are_nan_is_nan():
+    q, k, v = tensors(2, 3000, 4, 1, 128, 3)
+    k[40] = float("nan")
+    out, lse = api.attn_prefill_packed(q.cuda(), k.cuda(), v.cuda(), cumulative([2]).cuda(), cumulative([3000]).cuda(),
+                                       want_lse=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(out.float()).all() and torch.isnan(lse).all()
+
+
+def test_without_a_workspace_nothing_is_split():
+    """The C call with a NULL workspace gives the rows to one SM each; the result is as good."""
+    import ctypes
+
+    from scaled_dot_product_prefill_b200 import _lib
+
+    Hq, Hkv, D, lk = 8, 2, 128, [3000]
+    q, k, v = (x.cuda() for x in tensors(4, 3000, Hq, Hkv, D, 3))
+    cu_q, cu_k = cumulative([4]).cuda(), cumulative(lk).cuda()
+    out, lse = torch.empty_like(q), torch.empty((4, Hq), device="cuda")
+    st = _lib.load().attn_prefill_packed(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), 1, 4, 3000, Hq, Hkv, D, Hq * D,
+        Hkv * D, Hkv * D, Hq * D, D ** -0.5, 1, 0, None, 0, out.data_ptr(), lse.data_ptr(),
+        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert st == 0 and api.attn_device_status(clear=True) == 0
+    assert_packed((out, lse), packed_attention(f64(q), f64(k), f64(v), [0, 4], [0, 3000], D ** -0.5))
+
+
+def test_split_calls_in_two_replayed_graphs_do_not_share_their_workspaces():
+    Hq, Hkv, D = 8, 2, 128
+    q, k, v = (x.cuda() for x in tensors(8, 4000, Hq, Hkv, D, 3))
+    cu_k = cumulative([4000]).cuda()
+    graphs, outs, streams = [], [], []
+    for i in range(2):
+        cu = cumulative([8 - 3 * i]).cuda()
+        ws = torch.empty(api.attn_prefill_packed_workspace_size(1, 8, Hq, Hkv, D, 4000), dtype=torch.uint8, device="cuda")
+        out = torch.zeros_like(q)
+        fn = lambda: api.attn_prefill_packed(q, k, v, cu, cu_k, out=out, workspace=ws)  # noqa: E731, B023
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            fn()
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fn()
+        graphs.append((g, cu, ws)), outs.append((out, out.clone())), streams.append(s)
+    torch.cuda.synchronize()
+    want = [o.clone() for o, _ in outs]
+    for _ in range(5):
+        for o, _ in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for (g, _, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for (o, _), w in zip(outs, want))
+    assert api.attn_device_status(clear=True) == 0
+    del graphs

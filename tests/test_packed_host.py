@@ -17,15 +17,15 @@ def lib():
 
 
 def packed(q=FAKE, k=FAKE, v=FAKE, cu_q=FAKE, cu_k=FAKE, B=2, Tq=64, Tk=64, Hq=8, Hkv=2, D=64, qs=512, ks=128, vs=128,
-           os=512, scale=0.125, causal=1, window=0, out=FAKE, lse=None):
+           os=512, scale=0.125, causal=1, window=0, ws=None, ws_bytes=0, out=FAKE, lse=None):
     return lib().attn_prefill_packed(q, k, v, cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, qs, ks, vs, os, scale, causal, window,
-                                     out, lse, None)
+                                     ws, ws_bytes, out, lse, None)
 
 
 def paged(q=FAKE, kp=FAKE, vp=FAKE, cu_q=FAKE, pt=FAKE, sl=FAKE, page=16, B=2, Tq=64, Hq=8, Hkv=2, D=64, qs=512, os=512,
-          num_pages=8, max_pages=4, max_seq_len=64, scale=0.125, causal=1, window=0, out=FAKE, lse=None):
+          num_pages=8, max_pages=4, max_seq_len=64, scale=0.125, causal=1, window=0, ws=None, ws_bytes=0, out=FAKE, lse=None):
     return lib().attn_prefill_packed_paged(q, kp, vp, cu_q, pt, sl, page, B, Tq, Hq, Hkv, D, qs, os, num_pages, max_pages,
-                                           max_seq_len, scale, causal, window, out, lse, None)
+                                           max_seq_len, scale, causal, window, ws, ws_bytes, out, lse, None)
 
 
 BOTH = [
@@ -35,6 +35,7 @@ BOTH = [
     (dict(scale=float("inf")), 1), (dict(causal=2), 1), (dict(window=-1), 1), (dict(D=96, qs=768, os=768), 1),
     (dict(D=256, qs=2048, os=2048), 1),
     (dict(qs=504), 1), (dict(qs=516), 1), (dict(os=0), 1), (dict(qs=-512), 1), (dict(os=1 << 40), 1),
+    (dict(ws=OFF8, ws_bytes=1 << 30), 6),
     (dict(causal=0, window=4), 2), (dict(B=70000), 2), (dict(Tq=(1 << 30) + 1), 2),
     (dict(B=0, q=None, out=None, cu_q=None), 0), (dict(Tq=0, q=None, out=None), 0), (dict(Hq=0, q=None, out=None), 0),
 ]
@@ -60,6 +61,24 @@ def test_packed_prefill_refuses(change, status):
     (dict(num_pages=0x7FFFFFFF), 2), (dict(max_seq_len=(1 << 30) + 1), 2)])
 def test_packed_paged_prefill_refuses(change, status):
     assert paged(**change) == status
+
+
+def test_the_workspace_of_a_split():
+    size = lib().attn_prefill_packed_workspace_size
+    # few items and long sequences: 2 sequences x 2 head blocks of one block each
+    need = size(2, 10, 8, 2, 128, 8192)
+    assert need == 16 * 10 * 8 * (128 + 1) * 4                       # 16 parts at most
+    assert size(2, 10, 8, 2, 128, 600) == 5 * 10 * 8 * 129 * 4       # a part is one key tile at least
+    assert size(2, 10, 8, 2, 128, 384) == 0                          # 3 key tiles are not split
+    assert size(1, 1024, 8, 8, 64, 1024) == 2 * 1024 * 8 * 65 * 4    # full tiles: 4 key tiles a part
+    assert size(1, 1024, 8, 8, 64, 7 * 128) == 0
+    assert size(100, 100, 32, 8, 128, 8192) == 0                     # enough items without a split
+    for bad in ((0, 10, 8, 2, 128, 8192), (2, 0, 8, 2, 128, 8192), (2, 10, 8, 3, 128, 8192), (2, 10, 8, 2, 0, 8192),
+                (2, 10, 8, 2, 128, -1), (-1, 10, 8, 2, 128, 8192)):
+        assert size(*bad) == 0
+    kw = dict(Tq=10, D=128, qs=1024, os=1024)
+    assert paged(ws=FAKE, ws_bytes=need - 1, max_seq_len=8192, max_pages=512, **kw) == 6
+    assert packed(ws=FAKE, ws_bytes=need - 1, Tk=2 * 8192, ks=256, vs=256, **kw) == 6
 
 
 def append(fp8=False, q=FAKE, k=FAKE, v=FAKE, qo=FAKE, ko=None, kp=FAKE, vp=FAKE, table=FAKE, cu=FAKE, pt=FAKE, sl=FAKE,
