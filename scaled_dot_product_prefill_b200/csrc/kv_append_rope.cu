@@ -20,7 +20,10 @@
 // lane and the lane's 8 cosines and 8 sines serve all its STEPS rows.  All rows'
 // loads are issued before anything that depends on the position, whose
 // chain (sequence, length, then page and angles) is the latency of a
-// small call.
+// small call.  Blocks of 2 warps, 12 of them on an SM: 24 warps keep 96 KB of
+// loads in flight, where the registers of a free choice left 16 warps (130 us
+// on 30.6 k tokens, 768 MB, against 117 us, 6.5 TB/s, the measured copy rate), and
+// blocks of 8 warps end less evenly (24.6 us on 5.4 k tokens, 134 MB, against 23.3).
 #include <type_traits>
 
 #include "common.cuh"
@@ -29,7 +32,7 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 
 struct RopeParams {
   const __nv_bfloat16 *q, *k, *v;
@@ -95,7 +98,7 @@ __device__ __forceinline__ int ends_before(const int32_t* cu, int B, int t, int 
 }
 
 template <bool FP8, bool INTERLEAVED, int STEPS>
-__global__ void __launch_bounds__(kThreads) kv_append_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, STEPS > 1 ? 12 : 1) kv_append_rope_kernel(const RopeParams p) {
   grid_dependency_wait();   // the pools may still be read, and q, k, v written, by the kernel before
   grid_dependents_may_start();
   const int lane = threadIdx.x & 31;
@@ -251,7 +254,11 @@ cudaError_t launch(RopeParams& p, cudaStream_t stream) {
   const int steps = (p.Hq + 2 * p.Hkv + per - 1) / per;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const bool few = static_cast<long long>(p.T) * steps <= static_cast<long long>(sms) * 64;
+  // With few warp steps (decode steps, short prompts) each gets a warp, for the shortest chain; with many a
+  // warp takes 4, for its loads in flight and one position chain to them.  us with 1 and with 4 at 5, 21,
+  // 42 and 166 steps per SM (32/8 heads, D = 128, one decode step and 256 to 2048 tokens): 2.4 / 2.8,
+  // 3.5 / 3.0, 4.1 / 3.3, 13.3 / 7.6; at 9, 17 and 69 (12/12, D = 64): 2.4 / 2.8, 2.7 / 3.0, 6.0 / 5.7.
+  const bool few = static_cast<long long>(p.T) * steps <= static_cast<long long>(sms) * 16;
   const int take = few ? 1 : 4;
   p.groups = (steps + take - 1) / take;
   const long long warps = static_cast<long long>(p.T) * p.groups;
