@@ -488,12 +488,14 @@ def _shaped(t, name, shape, dtype):
     return t.data_ptr()
 
 
-def _on_device(tensors, names):
+def _on_device(*tensors):
     """The device index of every tensor that is not None: the current CUDA device."""
     dev = tensors[0].get_device()
-    for t, name in zip(tensors, names):
-        if t is not None and (t.get_device() != dev or dev < 0):
-            raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be CUDA tensors on the current device, got {dev=} and {t.device}")
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors on the current device")
     if dev != torch.cuda.current_device():
         raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
     return dev
@@ -536,6 +538,8 @@ def attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len) -> int:
 def _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, max_seq_len, device):
     """The workspace, its pointer and its size in bytes, and what was allocated here (sizes that never split need none)."""
     if workspace is None:
+        if max_seq_len <= 384:   # 3 key tiles are never split: spare short prompts the question
+            return None, None, 0, made
         need = _lib.load().attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len)
         if need == 0:
             return None, None, 0, made
@@ -575,8 +579,7 @@ def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True
     out, out_stride, lse, lse_ptr, made = _packed_results(q, Tq, Hq, D, out, lse, want_lse)
     workspace, ws_ptr, ws_bytes, made = _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, -(-Tk // max(B, 1)),
                                                           q.device)
-    dev = _on_device((q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace),
-                     ("q", "k", "v", "cu_seqlens_q", "cu_seqlens_k", "out", "lse", "workspace"))
+    dev = _on_device(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace)
     _check("attn_prefill_packed", _lib.load().attn_prefill_packed(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
         out_stride, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)), int(window),
@@ -609,8 +612,7 @@ def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_l
     out, out_stride, lse, lse_ptr, made = _packed_results(q, Tq, Hq, D, out, lse, want_lse)
     max_seq_len = int(max_seq_len)
     workspace, ws_ptr, ws_bytes, made = _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, max_seq_len, q.device)
-    dev = _on_device((q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, out, lse, workspace),
-                     ("q", "k_pool", "v_pool", "cu_seqlens_q", "page_table", "seq_lens", "out", "lse", "workspace"))
+    dev = _on_device(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, out, lse, workspace)
     _check("attn_prefill_packed_paged", _lib.load().attn_prefill_packed_paged(
         q.data_ptr(), kp, vp, cu_q, table, lens, page_size, B, Tq, Hq, Hkv, D, q_stride, out_stride, num_pages,
         max_pages, max_seq_len, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)),
@@ -659,9 +661,7 @@ def _append_rope(name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table,
         cu = _shaped(cu_seqlens, "cu_seqlens", (B + 1,), torch.int32)
     elif B and T % B:
         raise ValueError(f"without cu_seqlens the {T} tokens must be the same number of each of {B} sequences")
-    dev = _on_device((k, v, q, q_out, k_out, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens),
-                     ("k", "v", "q", "q_out", "k_out", "k_pool", "v_pool", "cos_sin", "page_table", "seq_lens",
-                      "cu_seqlens"))
+    dev = _on_device(k, v, q, q_out, k_out, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens)
     _check(name, getattr(_lib.load(), name)(
         q_ptr, k.data_ptr(), v.data_ptr(), q_out_ptr, k_out_ptr, kp, vp, angles, cu, table, lens, page_size, B, T, Hq,
         Hkv, D, rot, 1 if interleaved else 0, q_stride, k_stride, v_stride, q_out_stride, k_out_stride, num_pages,

@@ -994,35 +994,37 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         // (64 columns of the warp's 32 rows at a time; the 16-byte pieces of a row are permuted by its
         // number, which keeps both sides free of bank conflicts)
         uint8_t* stage = sOut + warp * 4096;
+        const int at0 = wq * 32 + (lane >> 3), piece = lane & 7, mask = (1 << p.pack_log2) - 1;
+        __nv_bfloat16* base = p.out + (static_cast<size_t>(it.q_base) + r0) * p.out_stride +
+                              (static_cast<size_t>(it.hb) << p.pack_log2) * D + piece * 8;
+        const int last = it.end - r0;   // tokens of this tile
 #pragma unroll 1
         for (int h = 0; h < D / 64; ++h) {
+          uint32_t o[64];
+          tmem_ld32(o_tmem + 64 * h, o);
+          tmem_ld32(o_tmem + 64 * h + 32, o + 32);
+          tmem_wait_ld();
           __syncwarp();   // the warp has read the half before
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_tmem + 64 * h + 32 * c, o);
-            tmem_wait_ld();
+          for (int e = 0; e < 8; ++e) {
+            uint32_t w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
-              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + e) ^ (lane & 7)) * 16)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int x = 0; x < 4; ++x)
+              w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
           __syncwarp();
+          uint4 u[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int row = 4 * e + (lane >> 3), piece = lane & 7;
-            const uint4 u = *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) * 16));
-            const int at = wq * 32 + row;                      // row within the tile
-            const int tok = r0 + (at >> p.pack_log2);
-            const int hd = (it.hb << p.pack_log2) + (at & ((1 << p.pack_log2) - 1));
-            if (tok < it.end)
-              *reinterpret_cast<uint4*>(p.out + (static_cast<size_t>(it.q_base) + tok) * p.out_stride +
-                                        static_cast<size_t>(hd) * D + 64 * h + piece * 8) = u;
+            const int row = 4 * e + (lane >> 3);
+            u[e] = *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) * 16));
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int at = at0 + 4 * e, tok = at >> p.pack_log2;
+            if (tok < last)
+              *reinterpret_cast<uint4*>(base + tok * p.out_stride + (at & mask) * D + 64 * h) = u[e];
           }
         }
       }
