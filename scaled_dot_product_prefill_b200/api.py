@@ -511,6 +511,11 @@ def _raw_stream(stream, dev, *made):
     return stream.cuda_stream
 
 
+def _c_int(x):
+    """x as the C int that says the same: beyond its range the largest, or a negative one (which is refused)."""
+    return max(-1, min(int(x), 0x7FFFFFFF))
+
+
 def _batch_of(cu, name):
     if cu.dim() != 1 or cu.shape[0] < 1:
         raise ValueError(f"{name} must have shape [B + 1], got {tuple(cu.shape)}")
@@ -582,7 +587,7 @@ def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True
     dev = _on_device(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace)
     _check("attn_prefill_packed", _lib.load().attn_prefill_packed(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
-        out_stride, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)), int(window),
+        out_stride, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)), _c_int(window),
         ws_ptr, ws_bytes, out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
     return out if lse is None else (out, lse)
 
@@ -610,13 +615,13 @@ def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_l
     table = _shaped(page_table, "page_table", (B, max_pages), torch.int32)
     lens = _shaped(seq_lens, "seq_lens", (B,), torch.int32)
     out, out_stride, lse, lse_ptr, made = _packed_results(q, Tq, Hq, D, out, lse, want_lse)
-    max_seq_len = int(max_seq_len)
+    max_seq_len = _c_int(max_seq_len)
     workspace, ws_ptr, ws_bytes, made = _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, max_seq_len, q.device)
     dev = _on_device(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, out, lse, workspace)
     _check("attn_prefill_packed_paged", _lib.load().attn_prefill_packed_paged(
         q.data_ptr(), kp, vp, cu_q, table, lens, page_size, B, Tq, Hq, Hkv, D, q_stride, out_stride, num_pages,
         max_pages, max_seq_len, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)),
-        int(window), ws_ptr, ws_bytes, out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
+        _c_int(window), ws_ptr, ws_bytes, out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
     return out if lse is None else (out, lse)
 
 

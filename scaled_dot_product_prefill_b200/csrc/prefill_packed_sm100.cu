@@ -107,7 +107,6 @@ struct Params {
   const int32_t* cu_k;      // the same for k and v (not PAGED)
   int pack_log2;            // s: 2^s query heads of a kv head share a tile
   int head_blocks;          // Hq >> s
-  int tiles;                // query tiles per item, 1 or 2
   // PAGED: K and V come from [num_pages, Hkv, page_size, D] pools through page_table [B, max_pages];
   // sequence b has seq_lens[b] keys (at most max_seq_len)
   const int32_t* page_table;
@@ -160,35 +159,46 @@ __device__ __forceinline__ PackedSpan packed_span(const Params& p, int b) {
   return s;
 }
 
-// How a sequence's query blocks (of 2^tb_log2 tokens) spread over cost levels.
-// Causal: block qb ends level qb + o, o = ceil((sk - sq) / block), whose last
-// visible key lies in key block level - 1; blocks that see no key or only
-// the first block's share level 0.  Not causal: all blocks cost the same, one
-// level by the number of keys.
-struct PackedLevels {
+// How a sequence's query blocks (of 2^tb_log2 tokens) spread over cost steps.
+// Causal: block qb ends at step qb + o, o = ceil((sk - sq) / block), whose last
+// visible key lies in key block step - 1; blocks that see no key or only
+// the first block's share step 0.  Not causal: all blocks cost the same, one
+// step by the number of keys.  A level is 2^shift steps.
+struct PackedSteps {
   int o, nb;
 };
 
-__device__ __forceinline__ PackedLevels packed_levels(const Params& p, const PackedSpan& s, int tb_log2) {
+__device__ __forceinline__ PackedSteps packed_steps(const Params& p, const PackedSpan& s, int tb_log2) {
   const int up = (1 << tb_log2) - 1;
-  PackedLevels l;
+  PackedSteps l;
   l.nb = (s.sq >> tb_log2) + ((s.sq & up) ? 1 : 0);
   l.o = p.causal ? ((s.sk - s.sq) >> tb_log2) + (((s.sk - s.sq) & up) ? 1 : 0)
                  : (s.sk >> tb_log2) + ((s.sk & up) ? 1 : 0);
   return l;
 }
 
-// Blocks of the sequence at level q >= 0, and its next level below q (-1: none).
-__device__ __forceinline__ int blocks_at(const PackedLevels& l, int causal, int q) {
-  if (!causal) return q == l.o ? l.nb : 0;
-  if (q > 0) return (q >= l.o && q < l.o + l.nb) ? 1 : 0;   // o + nb <= 2^30 + 1: no sum wraps
-  return min(max(1 - l.o, 0), l.nb);
+// The sequence's highest step (-1: no blocks), and its lowest.  o + nb <= 2^30 + 1: no sum here wraps.
+__device__ __forceinline__ int top_step(const PackedSteps& l, int causal) {
+  return l.nb == 0 ? -1 : causal ? max(l.o + l.nb - 1, 0) : l.o;
 }
-__device__ __forceinline__ int next_level(const PackedLevels& l, int causal, int q) {
+__device__ __forceinline__ int low_step(const PackedSteps& l) { return max(l.o, 0); }
+
+// Blocks of the sequence at level q >= 0, and its next level below q (-1: none).
+__device__ __forceinline__ int blocks_at(const PackedSteps& l, int causal, int q, int shift) {
+  if (!causal) return q == l.o >> shift ? l.nb : 0;
+  const int from = q << shift, to = from + (1 << shift);   // steps of the level
+  if (q == 0) return min(max(to - l.o, 0), l.nb);
+  return max(min(to, l.o + l.nb) - max(from, l.o), 0);
+}
+__device__ __forceinline__ int next_level(const PackedSteps& l, int causal, int q, int shift) {
   if (l.nb == 0) return -1;
-  if (!causal) return l.o < q ? l.o : -1;
-  const int n = min(q - 1, max(l.o + l.nb - 1, 0));
-  return n >= max(l.o, 0) ? n : -1;
+  const int n = min(q - 1, top_step(l, causal) >> shift);
+  return n >= low_step(l) >> shift ? n : -1;
+}
+// The j-th block of the sequence at level q, the costliest first.
+__device__ __forceinline__ int block_of(const PackedSteps& l, int causal, int q, int shift, int j) {
+  if (!causal) return j;
+  return min((q + 1) << shift, l.o + l.nb) - 1 - l.o - j;
 }
 
 // The key-tile ranges of an item's query tiles: those that hold a key some row sees.
@@ -668,10 +678,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     // ------------------------------------------------------------ item scheduler
     // Blocks are ranked level by level from the highest (costliest) down, within
     // a level by sequence; item k is head block k % head_blocks of the block of
-    // rank k / head_blocks.  This CTA's k only grow, so one walk down the levels
-    // serves all its items; a level costs a pass over the sequences, 32 at a time.
+    // rank k / head_blocks.  This CTA's k only grow, so one walk down the levels,
+    // and within a level over the sequences, serves all its items.  A level costs two
+    // passes over the sequences, 32 at a time: levels get wider (2^shift steps) until
+    // there are at most 2048 such chunks to visit in all.
     const int tpt = BM >> p.pack_log2;
-    const int tb_log2 = 7 - p.pack_log2 + (p.tiles - 1);
+    const int tb_log2 = 8 - p.pack_log2;   // NQ * BM rows of 2^s heads
     const int chunks = (p.B + 31) / 32;
     // sequence 32 c + lane; the first 32 stay in registers
     auto span_of = [&](int c) -> PackedSpan {
@@ -680,19 +692,29 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       return s;
     };
     const PackedSpan span0 = span_of(0);
-    auto levels_of = [&](int c) -> PackedLevels { return packed_levels(p, c == 0 ? span0 : span_of(c), tb_log2); };
+    auto steps_of = [&](int c) -> PackedSteps { return packed_steps(p, c == 0 ? span0 : span_of(c), tb_log2); };
     const int blocks_per_kv = p.Hq / p.Hkv >> p.pack_log2;   // head blocks of a kv head
-    int level = 0x7FFFFFFF, below = -1, base = 0, count = 0;
-    auto visit = [&](int q) {   // blocks at level q, and the next level that has any
+    int top = -1;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) top = max(top, top_step(steps_of(c), p.causal));
+    top = __reduce_max_sync(0xffffffffu, top);
+    int shift = 0;
+    while (shift < 20 && ((top >> shift) + 1LL) * chunks > 2048) ++shift;
+    // the level being dealt out: its blocks, the rank of its first, the next level, and how many of
+    // its blocks lie in chunks before `chunk`
+    int level = -1, count = 0, base = 0, below = -1, chunk = 0, passed = 0;
+    auto visit = [&](int q) {
       int m = 0, nx = -1;
+#pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
-        const PackedLevels l = levels_of(c);
-        m += blocks_at(l, p.causal, q);
-        nx = max(nx, next_level(l, p.causal, q));
+        const PackedSteps l = steps_of(c);
+        m += blocks_at(l, p.causal, q, shift);
+        nx = max(nx, next_level(l, p.causal, q, shift));
       }
       level = q;
       count = __reduce_add_sync(0xffffffffu, m);
       below = __reduce_max_sync(0xffffffffu, nx);
+      chunk = passed = 0;
     };
     // Two passes: the items with key tiles, then (if any) those none of whose rows sees a key, whose
     // zeros the softmax warps write.  The producer and the MMA thread look an item ahead, and
@@ -702,8 +724,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     bool go_on = true;
     for (int pass = 0; pass < (none ? 2 : 1) && go_on; ++pass) {
       const bool rows_left = pass == 1;
-      base = count = 0;
-      visit(0x7FFFFFFF);   // above every level: no blocks
+      base = 0;
+      level = -1;
+      if (top >= 0) visit(top >> shift);
       for (int r = 0;; ++r) {
         const int P = gridDim.x, c = blockIdx.x;
         const int k = r * P + ((r & 1) ? (P - 1 - c) : c);
@@ -722,16 +745,15 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           level = -1;
         }
         if (level >= 0) {
-          int j = rank - base;   // the j-th block of this level
-          for (int ch = 0; ch < chunks; ++ch) {
-            const PackedSpan sp = ch == 0 ? span0 : span_of(ch);
-            const PackedLevels l = packed_levels(p, sp, tb_log2);
-            const int m = blocks_at(l, p.causal, level);
+#pragma unroll 1
+          for (; chunk < chunks; ++chunk) {
+            int j = rank - base - passed;   // the j-th block of this level from this chunk on
+            const PackedSpan sp = chunk == 0 ? span0 : span_of(chunk);
+            const PackedSteps l = packed_steps(p, sp, tb_log2);
+            const int m = blocks_at(l, p.causal, level, shift);
             // inclusive count over the lanes: of ones where a sequence has one block at most
-            const bool ones = p.causal && level > 0;
-            const unsigned int set = __ballot_sync(0xffffffffu, m > 0);
-            int incl = __popc(set & (0xffffffffu >> (31 - lane)));
-            if (!ones) {
+            int incl = __popc(__ballot_sync(0xffffffffu, m > 0) & (0xffffffffu >> (31 - lane)));
+            if (__any_sync(0xffffffffu, m > 1)) {
               incl = m;
 #pragma unroll
               for (int d = 1; d < 32; d <<= 1) {
@@ -741,16 +763,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             }
             const int total = __shfl_sync(0xffffffffu, incl, 31);
             if (j >= total) {
-              j -= total;
+              passed += total;
               continue;
             }
             const int src = __ffs(__ballot_sync(0xffffffffu, incl > j)) - 1;
             j -= __shfl_sync(0xffffffffu, incl - m, src);
-            const int o = __shfl_sync(0xffffffffu, l.o, src), nb = __shfl_sync(0xffffffffu, l.nb, src);
-            const int qb = ones ? level - o : j;
+            const int qb = __shfl_sync(0xffffffffu, block_of(l, p.causal, level, shift, j), src);
+            const int nb = __shfl_sync(0xffffffffu, l.nb, src);
             // (counts of malformed, overlapping lengths may have wrapped: no block then)
-            if (src < 0 || ch * 32 + src >= p.B || qb < 0 || qb >= nb) break;
-            it.b = ch * 32 + src;
+            if (src < 0 || chunk * 32 + src >= p.B || qb < 0 || qb >= nb) break;
+            it.b = chunk * 32 + src;
             it.hb = unit - rank * p.head_blocks;
             it.g = blocks_per_kv == 1 ? it.hb : it.hb / blocks_per_kv;
             it.row0 = qb << tb_log2;
@@ -758,7 +780,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             it.k_base = __shfl_sync(0xffffffffu, sp.k0, src);
             it.sq = __shfl_sync(0xffffffffu, sp.sq, src);
             it.sk = __shfl_sync(0xffffffffu, sp.sk, src);
-            it.end = min(it.sq, it.row0 + p.tiles * tpt);
+            it.end = min(it.sq, it.row0 + NQ * tpt);
             packed_ranges(p, it);
             if constexpr (SPLIT) {
               cut_to_part(p, it, k - unit * p.splits);
@@ -998,6 +1020,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         __nv_bfloat16* base = p.out + (static_cast<size_t>(it.q_base) + r0) * p.out_stride +
                               (static_cast<size_t>(it.hb) << p.pack_log2) * D + piece * 8;
         const int last = it.end - r0;   // tokens of this tile
+        const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll 1
         for (int h = 0; h < D / 64; ++h) {
           uint32_t o[64];
@@ -1009,8 +1032,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           for (int e = 0; e < 8; ++e) {
             uint32_t w[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv, __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+            for (int x = 0; x < 4; ++x) {
+              float lo, hi;
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(o[8 * e + 2 * x]), __uint_as_float(o[8 * e + 2 * x + 1])), inv2), lo, hi);
+              w[x] = pack_bf16x2(lo, hi);
+            }
             *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
           __syncwarp();
@@ -1212,7 +1238,6 @@ bool packed_params(Params& p, void* out, float* lse, const int32_t* cu_q, int B,
   p.out_stride = out_stride;
   p.pack_log2 = pack_log2_of(Hq, Hkv);
   p.head_blocks = Hq >> p.pack_log2;
-  p.tiles = NQ;
   // the caller's workspace decides whether an item is split (none: never)
   p.splits = workspace != nullptr ? packed_splits(B, Tq, Hq, Hkv, max_seq_len) : 1;
   p.ws_o = static_cast<float*>(workspace);

@@ -108,6 +108,22 @@ def test_many_sequences_more_items_than_sms(D, window):
         assert torch.equal(one, got[0][a:e])
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_thousands_of_sequences_beside_a_long_one(causal):
+    """More sequences than one pass of the scheduler's warp holds, and steps of cost folded into levels."""
+    r = np.random.default_rng(8)
+    lens = r.integers(0, 5, 4000)
+    lens[1234], lens[3999] = 2500, 700
+    T, Hq, Hkv, D = int(lens.sum()), 4, 1, 64
+    q, k, v = (x.cuda() for x in tensors(T, T, Hq, Hkv, D, seed=5))
+    cu = cumulative(lens)
+    out, lse = api.attn_prefill_packed(q, k, v, cu.cuda(), causal=causal, want_lse=True)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 0
+    want = packed_attention(f64(q), f64(k), f64(v), cu.tolist(), cu.tolist(), D ** -0.5, causal)
+    assert_packed((out, lse), want)
+
+
 @pytest.mark.parametrize("D,Hq,Hkv,causal,window", [(64, 4, 4, True, 0), (128, 8, 2, True, 0), (128, 8, 2, True, 300),
                                                     (64, 4, 1, False, 0)])
 def test_equal_lengths_give_the_bits_of_the_dense_prefill(D, Hq, Hkv, causal, window):
@@ -327,6 +343,20 @@ def test_a_captured_graph_is_replayed_with_other_lengths_while_another_runs():
             torch.cuda.synchronize()
             assert torch.equal(eager, out)
     del graphs
+
+
+def test_arguments_beyond_a_c_int_mean_what_they_say_or_are_refused():
+    q, k, v = (x.cuda() for x in tensors(200, 200, 4, 2, 64, 60))
+    cu = cumulative([150, 50]).cuda()
+    want = api.attn_prefill_packed(q, k, v, cu)
+    assert torch.equal(api.attn_prefill_packed(q, k, v, cu, window=2 ** 32 + 5), want)
+    pool, table, lens = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16, device="cuda"), \
+        torch.zeros((2, 2), dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    for kw, status in ((dict(max_seq_len=2 ** 32 + 16), 2), (dict(max_seq_len=-2 ** 40), 1),
+                       (dict(max_seq_len=16, window=-2 ** 40), 1)):
+        with pytest.raises(api.AttnError) as e:
+            api.attn_prefill_packed_paged(q, pool, pool, cu, table, lens, **kw)
+        assert e.value.status == status
 
 
 def test_a_call_on_another_stream_with_its_own_result():
