@@ -517,9 +517,10 @@ def _c_int(x):
 
 
 def _batch_of(cu, name):
-    if cu.dim() != 1 or cu.shape[0] < 1:
-        raise ValueError(f"{name} must have shape [B + 1], got {tuple(cu.shape)}")
-    return cu.shape[0] - 1
+    size = cu.shape
+    if len(size) != 1 or size[0] < 1:
+        raise ValueError(f"{name} must have shape [B + 1], got {tuple(size)}")
+    return size[0] - 1
 
 
 def _packed_results(q, Tq, Hq, D, out, lse, want_lse):
@@ -567,10 +568,11 @@ def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True
     ceil(Tk / B)) bytes, allocated here if None.  Returns out, or (out, lse) with want_lse (or an lse tensor given);
     lse [Tq,Hq] fp32.
     """
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q, k and v must be [tokens, heads, D]")
-    Tq, Hq, D = q.shape
-    Tk, Hkv, _ = k.shape
+    try:
+        Tq, Hq, D = q.shape
+        Tk, Hkv, _ = k.shape
+    except ValueError:
+        raise ValueError("q, k and v must be [tokens, heads, D]") from None
     q_stride = _packed(q, "q", Tq, Hq, D)
     k_stride = _packed(k, "k", Tk, Hkv, D)
     v_stride = _packed(v, "v", Tk, Hkv, D)
@@ -601,13 +603,15 @@ def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_l
     Strides, rows of no sequence, the workspace (here for max_seq_len) and the result are as
     attn_prefill_packed's.
     """
-    if q.dim() != 3 or k_pool.dim() != 4 or page_table.dim() != 2:
-        raise ValueError("q must be [tokens,Hq,D], the pools [num_pages,Hkv,page_size,D], page_table [B,max_pages]")
-    Tq, Hq, D = q.shape
-    num_pages, Hkv, page_size, _ = k_pool.shape
+    try:
+        Tq, Hq, D = q.shape
+        num_pages, Hkv, page_size, _ = k_pool.shape
+        _, max_pages = page_table.shape
+    except ValueError:
+        raise ValueError("q must be [tokens,Hq,D], the pools [num_pages,Hkv,page_size,D], page_table "
+                         "[B,max_pages]") from None
     q_stride = _packed(q, "q", Tq, Hq, D)
     B = _batch_of(cu_seqlens_q, "cu_seqlens_q")
-    max_pages = page_table.shape[1]
     pool = (num_pages, Hkv, page_size, D)
     kp = _shaped(k_pool, "k_pool", pool, torch.bfloat16)
     vp = _shaped(v_pool, "v_pool", pool, torch.bfloat16)
@@ -625,22 +629,21 @@ def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_l
     return out if lse is None else (out, lse)
 
 
-def _append_rope(name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens, interleaved,
-                 q_out, k_out, stream, scales):
-    if k.dim() != 3 or k_pool.dim() != 4 or page_table.dim() != 2:
-        raise ValueError("k and v must be [tokens,Hkv,D], the pools [num_pages,Hkv,page_size,D], page_table "
-                         "[B,max_pages]")
-    T, Hkv, D = k.shape
-    num_pages, _, page_size, _ = k_pool.shape
-    B, max_pages = page_table.shape
+def _append_rope(fn, name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens,
+                 interleaved, q_out, k_out, stream, scales):
+    try:
+        T, Hkv, D = k.shape
+        num_pages, _, page_size, _ = k_pool.shape
+        B, max_pages = page_table.shape
+        Hq = 0 if q is None else q.shape[1]
+    except (ValueError, IndexError):
+        raise ValueError("q, k and v must be [tokens,heads,D], the pools [num_pages,Hkv,page_size,D], page_table "
+                         "[B,max_pages]") from None
     k_stride, v_stride = _packed(k, "k", T, Hkv, D), _packed(v, "v", T, Hkv, D)
-    Hq = q_stride = q_out_stride = k_out_stride = max_pos = rot = 0
+    q_stride = q_out_stride = k_out_stride = max_pos = rot = 0
     q_ptr = q_out_ptr = k_out_ptr = angles = cu = None
     made = ()
     if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [tokens, Hq, D]")
-        Hq = q.shape[1]
         q_stride = _packed(q, "q", T, Hq, D)
         if q_out is None:
             q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
@@ -655,11 +658,11 @@ def _append_rope(name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table,
     pool = (num_pages, Hkv, page_size, D)
     kp, vp = _shaped(k_pool, "k_pool", pool, pool_dtype), _shaped(v_pool, "v_pool", pool, pool_dtype)
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.shape[1] > D:
-            raise ValueError(f"cos_sin must have shape [max_pos, rot_dim] with at most {D} columns, got "
-                             f"{tuple(cos_sin.shape)}")
-        max_pos, rot = cos_sin.shape
-        angles = _shaped(cos_sin, "cos_sin", (max_pos, rot), torch.float32)
+        size = cos_sin.shape
+        if len(size) != 2 or size[1] > D:
+            raise ValueError(f"cos_sin must have shape [max_pos, rot_dim] with at most {D} columns, got {tuple(size)}")
+        max_pos, rot = size
+        angles = _shaped(cos_sin, "cos_sin", size, torch.float32)
     table = _shaped(page_table, "page_table", (B, max_pages), torch.int32)
     lens = _shaped(seq_lens, "seq_lens", (B,), torch.int32)
     if cu_seqlens is not None:
@@ -667,7 +670,7 @@ def _append_rope(name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table,
     elif B and T % B:
         raise ValueError(f"without cu_seqlens the {T} tokens must be the same number of each of {B} sequences")
     dev = _on_device(k, v, q, q_out, k_out, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens)
-    _check(name, getattr(_lib.load(), name)(
+    _check(name, fn(
         q_ptr, k.data_ptr(), v.data_ptr(), q_out_ptr, k_out_ptr, kp, vp, angles, cu, table, lens, page_size, B, T, Hq,
         Hkv, D, rot, 1 if interleaved else 0, q_stride, k_stride, v_stride, q_out_stride, k_out_stride, num_pages,
         max_pages, max_pos, *scales, _raw_stream(stream, dev, *made)))
@@ -685,15 +688,16 @@ def attn_kv_append_rope(q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, 
     pairs (c, c + rot_dim / 2), or (2c, 2c + 1) if interleaved.  q may be None; q_out may be q;
     k_out (optional, may be k) receives the rotated k.  Strides as attn_prefill_packed.
     """
-    return _append_rope("attn_kv_append_rope", torch.bfloat16, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens,
-                        cu_seqlens, interleaved, q_out, k_out, stream, ())
+    return _append_rope(_lib.load().attn_kv_append_rope, "attn_kv_append_rope", torch.bfloat16, q, k, v, k_pool, v_pool,
+                        cos_sin, page_table, seq_lens, cu_seqlens, interleaved, q_out, k_out, stream, ())
 
 
 def attn_kv_append_rope_fp8(q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, *, k_scale, v_scale,
                             cu_seqlens=None, interleaved=False, q_out=None, k_out=None, stream=None):
     """attn_kv_append_rope into uint8 E4M3 pools: code = nearest E4M3 to the fp32 value * (1/scale), ties to even."""
-    return _append_rope("attn_kv_append_rope_fp8", torch.uint8, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens,
-                        cu_seqlens, interleaved, q_out, k_out, stream, (float(k_scale), float(v_scale)))
+    return _append_rope(_lib.load().attn_kv_append_rope_fp8, "attn_kv_append_rope_fp8", torch.uint8, q, k, v, k_pool,
+                        v_pool, cos_sin, page_table, seq_lens, cu_seqlens, interleaved, q_out, k_out, stream,
+                        (float(k_scale), float(v_scale)))
 
 
 class PagePool:

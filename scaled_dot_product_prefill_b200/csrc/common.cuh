@@ -60,11 +60,6 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, s
 bool make_tensor_map_3d(CUtensorMap* m, const void* base, int elem_bytes, int inner, int rows, int planes,
                         int box_inner, int box_rows);
 
-// Tensor map over `rank` (at most 4) dimensions, innermost first, with 128-byte swizzle and zeros out of
-// bounds; strides: bytes between elements of dimensions 1 .. rank - 1.  False as above.
-bool encode_tensor_map(CUtensorMap* m, const void* base, int elem_bytes, int rank, const cuuint64_t* dims,
-                       const cuuint64_t* strides, const cuuint32_t* box);
-
 // Number of SMs of the current device (cached per device), 0 on error.
 int sm_count();
 
