@@ -661,6 +661,48 @@ attn_status_t attn_kv_append_rope_fp8(const void* q, const void* k, const void* 
                                       int num_pages, int max_pages, int max_pos,
                                       float k_scale, float v_scale, attn_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The packed calls with their arguments in one block.
+ *
+ * The same calls, checks and results; for bindings that pay for every argument
+ * they convert (ctypes: 2.7 us for the 27 of a rotating append, more than the
+ * append itself takes for a decode step; a block 0.5).  A block is read before
+ * the call returns and may be reused at once.  Fields are named as the
+ * arguments; pointers that a call has no use for are NULL.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct {
+  const void *q, *k, *v;                        /* paged: k_pool and v_pool in k and v */
+  const int32_t *cu_seqlens_q, *cu_seqlens_k;   /* cu_seqlens_k: not paged */
+  const int32_t *page_table, *seq_lens;         /* paged */
+  void *workspace, *out;
+  float *lse;
+  attn_stream_t stream;
+  uint64_t workspace_bytes;
+  int64_t q_stride, k_stride, v_stride, out_stride;
+  int32_t B, Tq, Tk, Hq, Hkv, D, causal, window;
+  int32_t page_size, num_pages, max_pages, max_seq_len;   /* paged */
+  float scale;
+  int32_t paged;                                /* 0: attn_prefill_packed, 1: attn_prefill_packed_paged */
+} attn_prefill_packed_args_t;
+
+attn_status_t attn_prefill_packed_args(const attn_prefill_packed_args_t* args);
+
+typedef struct {
+  const void *q, *k, *v;
+  void *q_out, *k_out, *k_pool, *v_pool;
+  const float* cos_sin;
+  const int32_t *cu_seqlens, *page_table, *seq_lens;
+  attn_stream_t stream;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  int32_t page_size, B, T, Hq, Hkv, D, rot_dim, interleaved, num_pages, max_pages, max_pos;
+  int32_t fp8;                                  /* 0: attn_kv_append_rope, 1: attn_kv_append_rope_fp8 */
+  float k_scale, v_scale;                       /* fp8 */
+} attn_kv_append_rope_args_t;
+
+attn_status_t attn_kv_append_rope_args(const attn_kv_append_rope_args_t* args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -516,6 +516,12 @@ def _c_int(x):
     return max(-1, min(int(x), 0x7FFFFFFF))
 
 
+def _c_float(x):
+    """x as a C float: beyond its range an infinity (which is refused)."""
+    x = float(x)
+    return x if abs(x) <= 3.4028234663852886e38 or x != x else math.copysign(math.inf, x)
+
+
 def _batch_of(cu, name):
     size = cu.shape
     if len(size) != 1 or size[0] < 1:
@@ -533,7 +539,7 @@ def _packed_results(q, Tq, Hq, D, out, lse, want_lse):
         lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
         made += (lse,)
     return (out, _packed(out, "out", Tq, Hq, D), lse,
-            None if lse is None else _shaped(lse, "lse", (Tq, Hq), torch.float32), made)
+            0 if lse is None else _shaped(lse, "lse", (Tq, Hq), torch.float32), made)
 
 
 def attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len) -> int:
@@ -542,13 +548,13 @@ def attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len) -> int:
 
 
 def _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, max_seq_len, device):
-    """The workspace, its pointer and its size in bytes, and what was allocated here (sizes that never split need none)."""
+    """The workspace (none for sizes that are not split), its pointer, its size in bytes, and what was allocated here."""
     if workspace is None:
         if max_seq_len <= 384:   # 3 key tiles are never split: spare short prompts the question
-            return None, None, 0, made
+            return None, 0, 0, made
         need = _lib.load().attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len)
         if need == 0:
-            return None, None, 0, made
+            return None, 0, 0, made
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         made += (workspace,)
     elif not workspace.is_contiguous():
@@ -587,10 +593,10 @@ def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True
     workspace, ws_ptr, ws_bytes, made = _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, -(-Tk // max(B, 1)),
                                                           q.device)
     dev = _on_device(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace)
-    _check("attn_prefill_packed", _lib.load().attn_prefill_packed(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q, cu_k, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
-        out_stride, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)), _c_int(window),
-        ws_ptr, ws_bytes, out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
+    _check("attn_prefill_packed", _lib.load().attn_prefill_packed_args(_lib.PACKED_ARGS.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q, cu_k, 0, 0, ws_ptr, out.data_ptr(), lse_ptr,
+        _raw_stream(stream, dev, *made), ws_bytes, q_stride, k_stride, v_stride, out_stride, B, Tq, Tk, Hq, Hkv, D,
+        1 if causal else 0, _c_int(window), 0, 0, 0, 0, 1.0 / math.sqrt(D) if scale is None else _c_float(scale), 0)))
     return out if lse is None else (out, lse)
 
 
@@ -622,15 +628,15 @@ def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_l
     max_seq_len = _c_int(max_seq_len)
     workspace, ws_ptr, ws_bytes, made = _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, max_seq_len, q.device)
     dev = _on_device(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, out, lse, workspace)
-    _check("attn_prefill_packed_paged", _lib.load().attn_prefill_packed_paged(
-        q.data_ptr(), kp, vp, cu_q, table, lens, page_size, B, Tq, Hq, Hkv, D, q_stride, out_stride, num_pages,
-        max_pages, max_seq_len, 1.0 / math.sqrt(D) if scale is None else float(scale), int(bool(causal)),
-        _c_int(window), ws_ptr, ws_bytes, out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made)))
+    _check("attn_prefill_packed_paged", _lib.load().attn_prefill_packed_args(_lib.PACKED_ARGS.pack(
+        q.data_ptr(), kp, vp, cu_q, 0, table, lens, ws_ptr, out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made),
+        ws_bytes, q_stride, 0, 0, out_stride, B, Tq, 0, Hq, Hkv, D, 1 if causal else 0, _c_int(window), page_size,
+        num_pages, max_pages, max_seq_len, 1.0 / math.sqrt(D) if scale is None else _c_float(scale), 1)))
     return out if lse is None else (out, lse)
 
 
-def _append_rope(fn, name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens,
-                 interleaved, q_out, k_out, stream, scales):
+def _append_rope(name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens,
+                 interleaved, q_out, k_out, stream, fp8=0, k_scale=1.0, v_scale=1.0):
     try:
         T, Hkv, D = k.shape
         num_pages, _, page_size, _ = k_pool.shape
@@ -641,7 +647,7 @@ def _append_rope(fn, name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_ta
                          "[B,max_pages]") from None
     k_stride, v_stride = _packed(k, "k", T, Hkv, D), _packed(v, "v", T, Hkv, D)
     q_stride = q_out_stride = k_out_stride = max_pos = rot = 0
-    q_ptr = q_out_ptr = k_out_ptr = angles = cu = None
+    q_ptr = q_out_ptr = k_out_ptr = angles = cu = 0
     made = ()
     if q is not None:
         q_stride = _packed(q, "q", T, Hq, D)
@@ -670,10 +676,10 @@ def _append_rope(fn, name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_ta
     elif B and T % B:
         raise ValueError(f"without cu_seqlens the {T} tokens must be the same number of each of {B} sequences")
     dev = _on_device(k, v, q, q_out, k_out, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens)
-    _check(name, fn(
-        q_ptr, k.data_ptr(), v.data_ptr(), q_out_ptr, k_out_ptr, kp, vp, angles, cu, table, lens, page_size, B, T, Hq,
-        Hkv, D, rot, 1 if interleaved else 0, q_stride, k_stride, v_stride, q_out_stride, k_out_stride, num_pages,
-        max_pages, max_pos, *scales, _raw_stream(stream, dev, *made)))
+    _check(name, _lib.load().attn_kv_append_rope_args(_lib.APPEND_ROPE_ARGS.pack(
+        q_ptr, k.data_ptr(), v.data_ptr(), q_out_ptr, k_out_ptr, kp, vp, angles, cu, table, lens,
+        _raw_stream(stream, dev, *made), q_stride, k_stride, v_stride, q_out_stride, k_out_stride, page_size, B, T, Hq,
+        Hkv, D, rot, 1 if interleaved else 0, num_pages, max_pages, max_pos, fp8, k_scale, v_scale)))
     return q_out
 
 
@@ -688,16 +694,15 @@ def attn_kv_append_rope(q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, 
     pairs (c, c + rot_dim / 2), or (2c, 2c + 1) if interleaved.  q may be None; q_out may be q;
     k_out (optional, may be k) receives the rotated k.  Strides as attn_prefill_packed.
     """
-    return _append_rope(_lib.load().attn_kv_append_rope, "attn_kv_append_rope", torch.bfloat16, q, k, v, k_pool, v_pool,
-                        cos_sin, page_table, seq_lens, cu_seqlens, interleaved, q_out, k_out, stream, ())
+    return _append_rope("attn_kv_append_rope", torch.bfloat16, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens,
+                        cu_seqlens, interleaved, q_out, k_out, stream)
 
 
 def attn_kv_append_rope_fp8(q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens, *, k_scale, v_scale,
                             cu_seqlens=None, interleaved=False, q_out=None, k_out=None, stream=None):
     """attn_kv_append_rope into uint8 E4M3 pools: code = nearest E4M3 to the fp32 value * (1/scale), ties to even."""
-    return _append_rope(_lib.load().attn_kv_append_rope_fp8, "attn_kv_append_rope_fp8", torch.uint8, q, k, v, k_pool,
-                        v_pool, cos_sin, page_table, seq_lens, cu_seqlens, interleaved, q_out, k_out, stream,
-                        (float(k_scale), float(v_scale)))
+    return _append_rope("attn_kv_append_rope_fp8", torch.uint8, q, k, v, k_pool, v_pool, cos_sin, page_table, seq_lens,
+                        cu_seqlens, interleaved, q_out, k_out, stream, 1, _c_float(k_scale), _c_float(v_scale))
 
 
 class PagePool:

@@ -247,7 +247,8 @@ attn_status_t attn_prefill_packed(const void* q, const void* k, const void* v, c
     return ATTN_ERR_WORKSPACE;
   return from_packed(attn::launch_prefill_tc_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, B, Tq, Tk, Hq, Hkv, D,
                                                     q_stride, k_stride, v_stride, out_stride, scale, causal,
-                                                    cut_window(window), workspace, out, lse, attn::device_error_word(),
+                                                    cut_window(window), workspace, out, lse,
+                                                    attn::device_error_word(),
                                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -614,6 +615,31 @@ attn_status_t attn_kv_append_rope_fp8(const void* q, const void* k, const void* 
   return kv_append_rope(q, k, v, q_out, k_out, k_pool, v_pool, cos_sin, cu_seqlens, page_table, seq_lens, page_size, B,
                         T, Hq, Hkv, D, rot_dim, interleaved, q_stride, k_stride, v_stride, q_out_stride, k_out_stride,
                         num_pages, max_pages, max_pos, stream, true, k_scale, v_scale);
+}
+
+}  // extern "C"
+
+extern "C" {
+
+attn_status_t attn_prefill_packed_args(const attn_prefill_packed_args_t* a) {
+  if (a == nullptr || (a->paged != 0 && a->paged != 1)) return ATTN_ERR_INVALID_ARG;
+  if (a->paged)
+    return attn_prefill_packed_paged(a->q, a->k, a->v, a->cu_seqlens_q, a->page_table, a->seq_lens, a->page_size, a->B,
+                                     a->Tq, a->Hq, a->Hkv, a->D, a->q_stride, a->out_stride, a->num_pages, a->max_pages,
+                                     a->max_seq_len, a->scale, a->causal, a->window, a->workspace, a->workspace_bytes,
+                                     a->out, a->lse, a->stream);
+  return attn_prefill_packed(a->q, a->k, a->v, a->cu_seqlens_q, a->cu_seqlens_k, a->B, a->Tq, a->Tk, a->Hq, a->Hkv,
+                             a->D, a->q_stride, a->k_stride, a->v_stride, a->out_stride, a->scale, a->causal, a->window,
+                             a->workspace, a->workspace_bytes, a->out, a->lse, a->stream);
+}
+
+attn_status_t attn_kv_append_rope_args(const attn_kv_append_rope_args_t* a) {
+  if (a == nullptr || (a->fp8 != 0 && a->fp8 != 1)) return ATTN_ERR_INVALID_ARG;
+  return kv_append_rope(a->q, a->k, a->v, a->q_out, a->k_out, a->k_pool, a->v_pool, a->cos_sin, a->cu_seqlens,
+                        a->page_table, a->seq_lens, a->page_size, a->B, a->T, a->Hq, a->Hkv, a->D, a->rot_dim,
+                        a->interleaved, a->q_stride, a->k_stride, a->v_stride, a->q_out_stride, a->k_out_stride,
+                        a->num_pages, a->max_pages, a->max_pos, a->stream, a->fp8 != 0, a->fp8 ? a->k_scale : 1.f,
+                        a->fp8 ? a->v_scale : 1.f);
 }
 
 }  // extern "C"

@@ -797,7 +797,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         if (it.b < 0 && none && !rows_left) break;   // the second pass ends the list
         const int slot = put % kItemRing;
-        if (!__all_sync(0xffffffffu, mbar_wait_idle(&item_empty[slot], ((put / kItemRing) & 1) ^ 1, abort_flag, p.err))) {
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait_idle(&item_empty[slot], ((put / kItemRing) & 1) ^ 1, abort_flag, p.err))) {
           go_on = false;
           break;
         }
@@ -1036,10 +1037,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               float lo, hi;
-              f2_unpack(f2_mul(f2_pack(__uint_as_float(o[8 * e + 2 * x]), __uint_as_float(o[8 * e + 2 * x + 1])), inv2), lo, hi);
+              const uint64_t pair = f2_pack(__uint_as_float(o[8 * e + 2 * x]), __uint_as_float(o[8 * e + 2 * x + 1]));
+              f2_unpack(f2_mul(pair, inv2), lo, hi);
               w[x] = pack_bf16x2(lo, hi);
             }
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) * 16)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
           __syncwarp();
           uint4 u[8];
@@ -1286,8 +1289,8 @@ cudaError_t launch_prefill_tc_packed(const void* q, const void* k, const void* v
                                      float scale, int causal, int window, void* workspace, void* out, float* lse,
                                      unsigned int* err, cudaStream_t stream) {
   Params p{};
-  if (!packed_params(p, out, lse, cu_q, B, Hq, Hkv, D, Tq, keys_each(Tk, B), out_stride, scale, causal, window, workspace,
-                     err))
+  if (!packed_params(p, out, lse, cu_q, B, Hq, Hkv, D, Tq, keys_each(Tk, B), out_stride, scale, causal, window,
+                     workspace, err))
     return cudaErrorNotSupported;
   p.cu_k = cu_k;
   p.Tk = Tk;
@@ -1297,7 +1300,8 @@ cudaError_t launch_prefill_tc_packed(const void* q, const void* k, const void* v
   const void* vb = Tk > 0 ? v : q;
   const int rows = Tk > 0 ? Tk : 1;
   if (!make_map_packed_q(&mq, q, D, Tq, p.head_blocks, p.pack_log2, q_stride) ||
-      !make_map_packed_kv(&mk, kb, D, rows, Hkv, k_stride, BN) || !make_map_packed_kv(&mv, vb, D, rows, Hkv, v_stride, BN))
+      !make_map_packed_kv(&mk, kb, D, rows, Hkv, k_stride, BN) ||
+      !make_map_packed_kv(&mv, vb, D, rows, Hkv, v_stride, BN))
     return cudaErrorInvalidValue;
   return D == 64 ? launch_d<64, false>(mq, mk, mv, p, stream) : launch_d<128, false>(mq, mk, mv, p, stream);
 }

@@ -353,7 +353,8 @@ def test_arguments_beyond_a_c_int_mean_what_they_say_or_are_refused():
     pool, table, lens = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16, device="cuda"), \
         torch.zeros((2, 2), dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
     for kw, status in ((dict(max_seq_len=2 ** 32 + 16), 2), (dict(max_seq_len=-2 ** 40), 1),
-                       (dict(max_seq_len=16, window=-2 ** 40), 1)):
+                       (dict(max_seq_len=16, window=-2 ** 40), 1), (dict(max_seq_len=16, scale=1e300), 1),
+                       (dict(max_seq_len=16, scale=float("nan")), 1)):
         with pytest.raises(api.AttnError) as e:
             api.attn_prefill_packed_paged(q, pool, pool, cu, table, lens, **kw)
         assert e.value.status == status

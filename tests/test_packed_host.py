@@ -111,6 +111,56 @@ def test_rotating_append_refuses(change, status, fp8):
     assert append(fp8, **change) == status
 
 
+def test_argument_blocks_are_laid_out_as_the_header_says(tmp_path):
+    """Sizes and offsets of the two blocks as a C compiler sees them, against the formats the binding packs."""
+    import os
+    import re
+    import shutil
+    import struct
+    import subprocess
+
+    from conftest import ROOT
+
+    header = os.path.join(ROOT, "include", "attn_b200.h")
+    text = re.sub(r"/\*.*?\*/", "", open(header).read(), flags=re.S)
+    src = ['#include "attn_b200.h"', "#include <stdio.h>", "#include <stddef.h>", "int main(void) {"]
+    for name in ("attn_prefill_packed_args_t", "attn_kv_append_rope_args_t"):
+        body = re.search(r"typedef struct \{([^}]*)\} " + name, text).group(1)
+        fields = re.findall(r"\b(\w+)\s*(?=[,;])", body)
+        src += [f'printf("{name} %zu", sizeof({name}));'] + [f'printf(" %zu", offsetof({name}, {f}));' for f in fields]
+        src += ['printf("\\n");']
+    (tmp_path / "a.c").write_text("\n".join(src + ["return 0; }"]))
+    cc = shutil.which("gcc") or shutil.which("cc")
+    subprocess.check_call([cc, "-I", os.path.dirname(header), str(tmp_path / "a.c"), "-o", str(tmp_path / "a")])
+    lines = subprocess.check_output([str(tmp_path / "a")], text=True).split("\n")
+    for line, fmt in zip(lines, (_lib.PACKED_ARGS, _lib.APPEND_ROPE_ARGS)):
+        size, *offsets = map(int, line.split()[1:])
+        codes = re.sub(r"(\d+)(\w)", lambda m: int(m.group(1)) * m.group(2), fmt.format)
+        assert size == fmt.size and len(codes) == len(offsets)
+        assert offsets == [struct.calcsize("=" + codes[:i]) for i in range(len(codes))]
+
+
+def test_argument_blocks_are_checked_as_the_calls():
+    f = lib().attn_kv_append_rope_args
+    base = dict(q=0x10000, k=0x10000, v=0x10000, qo=0x20000, ko=0, kp=0x10000, vp=0x10000, table=0x10000, cu=0, pt=0x10000,
+                sl=0x10000, stream=0, qs=512, ks=128, vs=128, qos=512, kos=0, page=16, B=2, T=6, Hq=8, Hkv=2, D=64, rot=64,
+                inter=0, num_pages=8, max_pages=4, max_pos=64, fp8=0, ksc=1.0, vsc=1.0)
+    call = lambda **kw: f(_lib.APPEND_ROPE_ARGS.pack(*{**base, **kw}.values()))  # noqa: E731
+    assert f(None) == 1
+    assert call(k=0) == 1 and call(fp8=2) == 1 and call(fp8=1, ksc=0.0) == 1 and call(rot=80) == 1 and call(page=12) == 2
+    assert call(B=0) == 0 and call(T=0) == 0
+    g = lib().attn_prefill_packed_args
+    pb = dict(q=0x10000, k=0x10000, v=0x10000, cu_q=0x10000, cu_k=0x10000, pt=0x10000, sl=0x10000, ws=0, out=0x20000, lse=0,
+              stream=0, ws_bytes=0, qs=512, ks=128, vs=128, os=512, B=2, Tq=6, Tk=6, Hq=8, Hkv=2, D=64, causal=1, window=0,
+              page=16, num_pages=8, max_pages=4, max_seq_len=64, scale=0.125, paged=0)
+    call = lambda **kw: g(_lib.PACKED_ARGS.pack(*{**pb, **kw}.values()))  # noqa: E731
+    assert g(None) == 1 and call(paged=2) == 1
+    for paged_ in (0, 1):
+        assert call(paged=paged_, q=0) == 1 and call(paged=paged_, D=96) == 1 and call(paged=paged_, B=70000) == 2
+        assert call(paged=paged_, Tq=0) == 0
+    assert call(cu_k=0) == 1 and call(paged=1, sl=0) == 1 and call(paged=1, page=48) == 2
+
+
 @pytest.mark.parametrize("scales", [(0.0, 1.0), (1.0, -1.0), (float("nan"), 1.0), (1.0, float("inf"))])
 def test_rotating_append_refuses_bad_scales(scales):
     assert append(True, scales=scales) == 1
