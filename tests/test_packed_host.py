@@ -63,6 +63,13 @@ def test_packed_paged_prefill_refuses(change, status):
     assert paged(**change) == status
 
 
+def test_the_workspace_of_sizes_that_no_call_takes_is_none():
+    size = lib().attn_prefill_packed_workspace_size
+    assert size(2, 10, 8, 2, 128, 1 << 30) > 0
+    for max_seq_len in ((1 << 30) + 1, 0x7FFFFFFF, -1):
+        assert size(2, 10, 8, 2, 128, max_seq_len) == 0
+
+
 def test_the_workspace_of_a_split():
     size = lib().attn_prefill_packed_workspace_size
     # few items and long sequences: 2 sequences x 2 head blocks of one block each
