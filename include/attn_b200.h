@@ -626,7 +626,7 @@ attn_status_t attn_kv_append_fp8(const void* k_new, const void* v_new, uint8_t* 
  *         (T a multiple of B; one decode step is T = B)
  * page_table [B, max_pages], seq_lens [B], page_size (a multiple of 8) : as
  *         attn_kv_append
- * D a multiple of 16, at most 512; rot_dim a multiple of 16, 0 .. D (0: a plain
+ * B at most 2^30; D a multiple of 16, at most 512; rot_dim a multiple of 16, 0 .. D (0: a plain
  *         packed append, cos_sin may be NULL).
  * Rows that no sequence holds, and tokens at positions below 0, are skipped:
  * nothing is written for them.  A position from max_pos on is skipped and

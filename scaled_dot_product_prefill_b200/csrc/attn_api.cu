@@ -584,6 +584,7 @@ attn_status_t kv_append_rope(const void* q, const void* k, const void* v, void* 
   if ((Hq > 0 && q_out == q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride))
     return ATTN_ERR_INVALID_ARG;
   if (D % 16 != 0 || D > 512 || rot_dim % 16 != 0 || page_size % 8 != 0) return ATTN_ERR_UNSUPPORTED;
+  if (B > (1 << 30)) return ATTN_ERR_UNSUPPORTED;   // the search for a token's sequence steps past B in int32
   if (rot_dim == 0) max_pos = 0x7FFFFFFF;   // no angles to run out of
   return from_cuda(attn::launch_kv_append_rope(
       q, k, v, q_out, k_out, k_pool, v_pool, cos_sin, cu_seqlens, page_table, seq_lens, page_size, B, T, Hq, Hkv, D,

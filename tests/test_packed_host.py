@@ -107,7 +107,7 @@ APPEND = [
     (dict(qs=500), 1), (dict(ks=64), 1), (dict(vs=129), 1), (dict(qos=0), 1), (dict(ko=FAKE, k=ctypes.c_void_p(0x20000), kos=0), 1),
     (dict(q=FAKE, qo=FAKE, qos=1024), 1), (dict(ko=FAKE, k=FAKE, kos=256), 1),
     (dict(D=72, rot=64, qs=576, qos=576, ks=144, vs=144), 2), (dict(D=528, qs=4224, qos=4224, ks=1056, vs=1056), 2),
-    (dict(rot=24), 2), (dict(page=12), 2),
+    (dict(rot=24), 2), (dict(page=12), 2), (dict(B=(1 << 30) + 1), 2), (dict(B=0x7FFFFFFF), 2),
     (dict(B=0, k=None), 0), (dict(T=0, k=None), 0), (dict(Hkv=0, k=None), 0),
 ]
 
