@@ -629,7 +629,12 @@ attn_status_t attn_kv_append_fp8(const void* k_new, const void* v_new, uint8_t* 
  * B at most 2^30; D a multiple of 16, at most 512; rot_dim a multiple of 16, 0 .. D (0: a plain
  *         packed append, cos_sin may be NULL).
  * Rows that no sequence holds, and tokens at positions below 0, are skipped:
- * nothing is written for them.  A position from max_pos on is skipped and
+ * nothing is written for them.  A cumulative length that decreases, is
+ * negative or passes T is reported as ATTN_ERR_BAD_PAGE by attn_device_status,
+ * and no row of a sequence that begins or ends outside the buffer is written:
+ * its positions count from an end that is not there.  Of two sequences that such
+ * an array gives a row to, one at most has it written.  A position from
+ * max_pos on is skipped and
  * reported as ATTN_ERR_BAD_PAGE by attn_device_status; so is, for the pools
  * alone, one that has no valid page.  Two tokens that land in the same slot
  * (pages shared by sequences that both append to them) leave either's values.

@@ -44,6 +44,7 @@ struct RopeParams {
   long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
   int B, T, n_each, Hq, Hkv, D, R, page_size, num_pages, max_pages, max_pos;
   int groups;                             // warps per token
+  long long row_warps;                    // T * groups
   float k_inv, v_inv;
 };
 
@@ -103,8 +104,13 @@ __global__ void __launch_bounds__(kThreads, STEPS > 1 ? 12 : 1) kv_append_rope_k
   grid_dependents_may_start();
   const int lane = threadIdx.x & 31;
   const long long w = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+  if (w >= p.row_warps) {   // the warps behind those of the rows look the lengths over, 32 sequences each
+    const long long b = (w - p.row_warps) * 32 + lane;
+    if (p.cu != nullptr && b < p.B && (p.cu[b] < 0 || p.cu[b + 1] < p.cu[b] || p.cu[b + 1] > p.T))
+      record_error(p.err, ATTN_ERRBIT_BADPAGE);
+    return;
+  }
   const int t = static_cast<int>(w / p.groups);
-  if (t >= p.T) return;
   const int group = static_cast<int>(w - static_cast<long long>(t) * p.groups);
 
   const int U = p.D / 16, per = 32 / U;            // lanes per row, rows per step
@@ -138,8 +144,9 @@ __global__ void __launch_bounds__(kThreads, STEPS > 1 ? 12 : 1) kv_append_rope_k
     if (seq >= p.B) return;
     first = p.cu[seq];
     end = p.cu[seq + 1];
-    if (t < first || t >= end) {
-      if (t >= p.cu[0] && lane == 0) record_error(p.err, ATTN_ERRBIT_BADPAGE);   // the lengths decrease somewhere
+    // positions count from the sequence's end: one that is not wholly in the buffer has none to go by
+    if (t < first || t >= end || first < 0 || end > p.T) {
+      if (t >= p.cu[0] && lane == 0) record_error(p.err, ATTN_ERRBIT_BADPAGE);
       return;
     }
   }
@@ -261,7 +268,9 @@ cudaError_t launch(RopeParams& p, cudaStream_t stream) {
   const bool few = static_cast<long long>(p.T) * steps <= static_cast<long long>(sms) * 16;
   const int take = few ? 1 : 4;
   p.groups = (steps + take - 1) / take;
-  const long long warps = static_cast<long long>(p.T) * p.groups;
+  p.row_warps = static_cast<long long>(p.T) * p.groups;
+  // (looking the lengths over in the rows' own warps slowed those: 127 us on 30.6 k tokens, against 120)
+  const long long warps = p.row_warps + (p.cu != nullptr ? (p.B + 31LL) / 32 : 0);
   const long long blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   auto kern = few ? kv_append_rope_kernel<FP8, INTERLEAVED, 1> : kv_append_rope_kernel<FP8, INTERLEAVED, 4>;

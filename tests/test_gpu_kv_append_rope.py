@@ -276,6 +276,55 @@ def test_malformed_cumulative_lengths_stay_in_the_buffers(cu):
     assert (out[:100] == 9).all() and (out[180:] == 9).all()
 
 
+def decreasing_among(B, at):
+    """Cumulative lengths of B sequences of 2 tokens; the one that ends sequence `at` is 3 lower than it was."""
+    cu = list(range(0, 2 * B + 1, 2))
+    cu[at + 1] -= 3
+    return cu
+
+
+@pytest.mark.parametrize("cu", [
+    [0, 30, 60, 85], [0, 30, 60, 81], [0, 30, 60, 4000], [0, 30, 80, 85],       # past the 80 rows, by a little or wholly
+    [0, 85, 90, 95], [81, 90, 95, 99], [-7, 30, 60, 80], [-3, 0, 40, 80], [-9, -5, 30, 80],
+    [0, 50, 20, 80], [0, 2 ** 31 - 1, 5, -2 ** 31], [0, 30, 60, 2 ** 31 - 1],
+    decreasing_among(40, 17), decreasing_among(40, 33), decreasing_among(40, 39)], ids=lambda cu: str(cu[:4]) + f"x{len(cu) - 1}")
+def test_malformed_cumulative_lengths_are_reported_and_write_no_wrong_slot(cu):
+    """Every malformed array is reported, and a row goes to the slot of a sequence that holds it within the
+    buffer, or nowhere."""
+    T, Hq, Hkv, D, page, B = 80, 4, 2, 64, 16, len(cu) - 1
+    lens = [100 + b % 3 for b in range(B)]
+    p = inputs.paged_inputs(B, 1, Hkv, D, page, 4, seq_lens=lens)
+    q, k, v = inputs.normal((T, Hq, D), 1), inputs.normal((T, Hkv, D), 2), inputs.normal((T, Hkv, D), 3)
+    kp, vp = p.k_pool.cuda(), p.v_pool.cuda()
+    q_out, k_out = (torch.full((T, h, D), 7.0, dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv))
+    api.attn_device_status(clear=True)
+    api.attn_kv_append_rope(q.cuda(), k.cuda(), v.cuda(), kp, vp, cos_sin_table(110, D).cuda(), p.page_table.cuda(),
+                            p.seq_lens.cuda(), cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                            q_out=q_out, k_out=k_out)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 5
+    # where each row may have gone
+    slots, held = {}, np.zeros(T, bool)
+    for b in range(B):
+        if 0 <= cu[b] <= cu[b + 1] <= T:
+            for t in range(cu[b], cu[b + 1]):
+                x, held[t] = lens[b] - cu[b + 1] + t, True
+                slots.setdefault((int(p.page_table[b, x // page]), x % page), set()).add(t)
+    before, after = bits(p.v_pool), bits(vp)
+    for pg, s in np.argwhere((before != after).any((1, 3))):
+        assert any(np.array_equal(after[pg, :, s], bits(v)[t]) for t in slots.get((pg, s), ())), (pg, s)
+    assert (q_out.cpu()[~held] == 7).all() and (k_out.cpu()[~held] == 7).all()
+    # rows of one sequence alone, which none of the malformed ones claims, are written
+    claims = np.zeros(T, int)
+    for b in range(B):
+        lo, hi = sorted((min(max(cu[b], 0), T), min(max(cu[b + 1], 0), T)))
+        claims[lo:hi] += 1
+    for (pg, s), rows in slots.items():
+        for t in rows:
+            if claims[t] == 1:
+                assert np.array_equal(after[pg, :, s], bits(v)[t]), t
+
+
 def test_far_positions_take_their_angles_from_the_table():
     """The last positions of a long cache: the pages in between are not touched, the angles are the table's."""
     Hq, Hkv, D, page, L = 4, 1, 64, 256, 1_000_003
