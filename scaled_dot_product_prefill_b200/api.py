@@ -501,14 +501,25 @@ def _on_device(*tensors):
     return dev
 
 
-def _raw_stream(stream, dev, *made):
-    """The stream handle; tensors made here on the current stream for a call on another are kept from early reuse."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    if made and stream != torch.cuda.current_stream():
-        for t in made:
-            t.record_stream(stream)
-    return stream.cuda_stream
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _new(shape, dtype, like, stream, returned=True):
+    """A tensor on like's device for a call on `stream` (None: the current stream).
+
+    It is allocated on the stream that writes it: a block of the current stream may still be in use by work
+    queued there, which a call on another stream does not wait for.  One that is returned is likely to be
+    read on the current stream, whose uses up to its release are waited for before its block is used again.
+    """
+    if stream is None or not like.is_cuda:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    here = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if returned:
+        t.record_stream(here)
+    return t
 
 
 def _c_int(x):
@@ -529,17 +540,14 @@ def _batch_of(cu, name):
     return size[0] - 1
 
 
-def _packed_results(q, Tq, Hq, D, out, lse, want_lse):
-    """out, its token stride, lse, its pointer, and what was allocated for them here."""
-    made = ()
+def _packed_results(q, Tq, Hq, D, out, lse, want_lse, stream):
+    """out, its token stride, lse and its pointer."""
     if out is None:
-        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
-        made = (out,)
+        out = _new((Tq, Hq, D), torch.bfloat16, q, stream)
     if lse is None and want_lse:
-        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
-        made += (lse,)
+        lse = _new((Tq, Hq), torch.float32, q, stream)
     return (out, _packed(out, "out", Tq, Hq, D), lse,
-            0 if lse is None else _shaped(lse, "lse", (Tq, Hq), torch.float32), made)
+            0 if lse is None else _shaped(lse, "lse", (Tq, Hq), torch.float32))
 
 
 def attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len) -> int:
@@ -547,19 +555,18 @@ def attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len) -> int:
                                                               int(max_seq_len)))
 
 
-def _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, max_seq_len, device):
-    """The workspace (none for sizes that are not split), its pointer, its size in bytes, and what was allocated here."""
+def _packed_workspace(workspace, B, Tq, Hq, Hkv, D, max_seq_len, q, stream):
+    """The workspace (none for sizes that are not split), its pointer and its size in bytes."""
     if workspace is None:
         if max_seq_len <= 384:   # 3 key tiles are never split: spare short prompts the question
-            return None, 0, 0, made
+            return None, 0, 0
         need = _lib.load().attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len)
         if need == 0:
-            return None, 0, 0, made
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        made += (workspace,)
+            return None, 0, 0
+        workspace = _new(need, torch.uint8, q, stream, returned=False)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size(), made
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True, window=0, scale=None, out=None,
@@ -589,13 +596,12 @@ def attn_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal=True
         cu_seqlens_k = cu_seqlens_q
     cu_q = _shaped(cu_seqlens_q, "cu_seqlens_q", (B + 1,), torch.int32)
     cu_k = _shaped(cu_seqlens_k, "cu_seqlens_k", (B + 1,), torch.int32)
-    out, out_stride, lse, lse_ptr, made = _packed_results(q, Tq, Hq, D, out, lse, want_lse)
-    workspace, ws_ptr, ws_bytes, made = _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, -(-Tk // max(B, 1)),
-                                                          q.device)
+    out, out_stride, lse, lse_ptr = _packed_results(q, Tq, Hq, D, out, lse, want_lse, stream)
+    workspace, ws_ptr, ws_bytes = _packed_workspace(workspace, B, Tq, Hq, Hkv, D, -(-Tk // max(B, 1)), q, stream)
     dev = _on_device(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, workspace)
     _check("attn_prefill_packed", _lib.load().attn_prefill_packed_args(_lib.PACKED_ARGS.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q, cu_k, 0, 0, ws_ptr, out.data_ptr(), lse_ptr,
-        _raw_stream(stream, dev, *made), ws_bytes, q_stride, k_stride, v_stride, out_stride, B, Tq, Tk, Hq, Hkv, D,
+        _raw_stream(stream, dev), ws_bytes, q_stride, k_stride, v_stride, out_stride, B, Tq, Tk, Hq, Hkv, D,
         1 if causal else 0, _c_int(window), 0, 0, 0, 0, 1.0 / math.sqrt(D) if scale is None else _c_float(scale), 0)))
     return out if lse is None else (out, lse)
 
@@ -624,12 +630,12 @@ def attn_prefill_packed_paged(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_l
     cu_q = _shaped(cu_seqlens_q, "cu_seqlens_q", (B + 1,), torch.int32)
     table = _shaped(page_table, "page_table", (B, max_pages), torch.int32)
     lens = _shaped(seq_lens, "seq_lens", (B,), torch.int32)
-    out, out_stride, lse, lse_ptr, made = _packed_results(q, Tq, Hq, D, out, lse, want_lse)
+    out, out_stride, lse, lse_ptr = _packed_results(q, Tq, Hq, D, out, lse, want_lse, stream)
     max_seq_len = _c_int(max_seq_len)
-    workspace, ws_ptr, ws_bytes, made = _packed_workspace(workspace, made, B, Tq, Hq, Hkv, D, max_seq_len, q.device)
+    workspace, ws_ptr, ws_bytes = _packed_workspace(workspace, B, Tq, Hq, Hkv, D, max_seq_len, q, stream)
     dev = _on_device(q, k_pool, v_pool, cu_seqlens_q, page_table, seq_lens, out, lse, workspace)
     _check("attn_prefill_packed_paged", _lib.load().attn_prefill_packed_args(_lib.PACKED_ARGS.pack(
-        q.data_ptr(), kp, vp, cu_q, 0, table, lens, ws_ptr, out.data_ptr(), lse_ptr, _raw_stream(stream, dev, *made),
+        q.data_ptr(), kp, vp, cu_q, 0, table, lens, ws_ptr, out.data_ptr(), lse_ptr, _raw_stream(stream, dev),
         ws_bytes, q_stride, 0, 0, out_stride, B, Tq, 0, Hq, Hkv, D, 1 if causal else 0, _c_int(window), page_size,
         num_pages, max_pages, max_seq_len, 1.0 / math.sqrt(D) if scale is None else _c_float(scale), 1)))
     return out if lse is None else (out, lse)
@@ -648,12 +654,10 @@ def _append_rope(name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table,
     k_stride, v_stride = _packed(k, "k", T, Hkv, D), _packed(v, "v", T, Hkv, D)
     q_stride = q_out_stride = k_out_stride = max_pos = rot = 0
     q_ptr = q_out_ptr = k_out_ptr = angles = cu = 0
-    made = ()
     if q is not None:
         q_stride = _packed(q, "q", T, Hq, D)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-            made = (q_out,)
+            q_out = _new((T, Hq, D), torch.bfloat16, q, stream)
         q_out_stride = _packed(q_out, "q_out", T, Hq, D)
         q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
@@ -678,7 +682,7 @@ def _append_rope(name, pool_dtype, q, k, v, k_pool, v_pool, cos_sin, page_table,
     dev = _on_device(k, v, q, q_out, k_out, k_pool, v_pool, cos_sin, page_table, seq_lens, cu_seqlens)
     _check(name, _lib.load().attn_kv_append_rope_args(_lib.APPEND_ROPE_ARGS.pack(
         q_ptr, k.data_ptr(), v.data_ptr(), q_out_ptr, k_out_ptr, kp, vp, angles, cu, table, lens,
-        _raw_stream(stream, dev, *made), q_stride, k_stride, v_stride, q_out_stride, k_out_stride, page_size, B, T, Hq,
+        _raw_stream(stream, dev), q_stride, k_stride, v_stride, q_out_stride, k_out_stride, page_size, B, T, Hq,
         Hkv, D, rot, 1 if interleaved else 0, num_pages, max_pages, max_pos, fp8, k_scale, v_scale)))
     return q_out
 

@@ -481,3 +481,30 @@ def test_split_calls_in_two_replayed_graphs_do_not_share_their_workspaces():
         assert all(torch.equal(o, w) for (o, _), w in zip(outs, want))
     assert api.attn_device_status(clear=True) == 0
     del graphs
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_call_on_another_stream_is_not_overwritten_by_work_queued_on_this_one(D):
+    """The current stream still has to fill blocks that were released on the host: no result or workspace made
+    by a call on another stream may lie in them."""
+    Hq, Hkv, n, L = 8, 2, 16, 3000
+    q, k, v = (x.cuda() for x in tensors(n, L, Hq, Hkv, D, 3))
+    cu_q, cu_k = cumulative([n]).cuda(), cumulative([L]).cuda()
+    want = api.attn_prefill_packed(q, k, v, cu_q, cu_k, want_lse=True)
+    p = inputs.paged_inputs(1, Hq, Hkv, D, 16, seed=3, seq_lens=[L])
+    kp, vp, pt, sl = (x.cuda() for x in (p.k_pool, p.v_pool, p.page_table, p.seq_lens))
+    kn, vn = k[:n].clone(), v[:n].clone()
+    turned = api.attn_kv_append_rope(q, kn, vn, kp, vp, None, pt, sl)
+    s = torch.cuda.Stream()
+    need = api.attn_prefill_packed_workspace_size(1, n, Hq, Hkv, D, L)
+    assert need > 0
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)             # some 50 ms
+    for _ in range(2):
+        for size in (q.numel() * 2, n * Hq * 4, need):
+            torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    out, lse = api.attn_prefill_packed(q, k, v, cu_q, cu_k, want_lse=True, stream=s)
+    again = api.attn_kv_append_rope(q, kn, vn, kp, vp, None, pt, sl, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(again, turned)
+    assert api.attn_device_status(clear=True) == 0

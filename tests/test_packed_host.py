@@ -238,3 +238,63 @@ def test_the_binding_refuses_append_tensors():
             api.attn_kv_append_rope(*args, **kw)
     with pytest.raises(ValueError, match="k_pool must be"):
         api.attn_kv_append_rope_fp8(q, k, k, pool, pool, tab, pt, sl, k_scale=1, v_scale=1)
+
+
+class OnCard(torch.Tensor):
+    """A host tensor that says it is on the card, for calls whose library and streams are stand-ins."""
+    is_cuda = property(lambda self: True)
+
+
+def on_card(x):
+    return torch.Tensor._make_subclass(OnCard, x)
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    """Stand-ins for streams and the library: (stream, every torch.empty's stream, every record_stream)."""
+    import contextlib
+
+    class Stream:
+        cuda_stream = 7
+
+    now, made, recorded, empty = ["current"], [], [], torch.empty
+
+    @contextlib.contextmanager
+    def entered(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 4096 if name.endswith("workspace_size") else 0
+
+    monkeypatch.setattr(torch.cuda, "stream", entered)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[-1])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((tuple(t.shape), s)))
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: made.append(now[-1]) or empty(*a, **kw))
+    monkeypatch.setattr(api, "_on_device", lambda *ts: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0)
+    monkeypatch.setattr(_lib, "load", Lib)
+    return Stream(), made, recorded
+
+
+def test_what_a_packed_call_allocates_comes_from_its_stream(streams):
+    """A block of the current stream may still be written by work queued there, which the call's stream does not
+    wait for; and what is returned may be read on the current stream until it is released."""
+    stream, made, recorded = streams
+    q, k, pool = on_card(t(600, 8, 64)), on_card(t(600, 2, 64)), on_card(t(4, 2, 16, 64))
+    res = [((600, 8, 64), "current"), ((600, 8), "current")]
+    api.attn_prefill_packed(q, k, k, i32(2), want_lse=True, stream=stream)
+    assert made == [stream] * 3 and recorded == res           # out, lse, workspace
+    del made[:], recorded[:]
+    api.attn_prefill_packed_paged(q, pool, pool, i32(2), i32(1, 40), i32(1), max_seq_len=600, want_lse=True, stream=stream)
+    assert made == [stream] * 3 and recorded == res
+    del made[:], recorded[:]
+    api.attn_kv_append_rope(q, k, k, pool, pool, None, i32(1, 40), i32(1), stream=stream)
+    assert made == [stream] and recorded == res[:1]
+    del made[:], recorded[:]
+    for kw in (dict(out=t(600, 8, 64), lse=t(600, 8, dtype=torch.float32), workspace=t(4096), stream=stream), {}):
+        api.attn_prefill_packed(q, k, k, i32(2), **kw)
+    assert made == ["current"] * 2 and not recorded           # without a stream: out and workspace on the current one
