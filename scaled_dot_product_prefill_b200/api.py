@@ -29,6 +29,23 @@ def _stream(stream):
     return ctypes_void(stream.cuda_stream)
 
 
+def _new(shape, dtype, like, stream, returned=True):
+    """A tensor on like's device for a call on `stream` (None: the current stream).
+
+    It is allocated on the stream that writes it: a block of the current stream may still be in use by work
+    queued there, which a call on another stream does not wait for.  One that is returned is likely to be
+    read on the current stream, whose uses up to its release are waited for before its block is used again.
+    """
+    if stream is None or not like.is_cuda:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    here = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    if returned:
+        t.record_stream(here)
+    return t
+
+
 def ctypes_void(x):
     import ctypes
 
@@ -85,7 +102,7 @@ def _prefill(name, dtype, q, k, v, causal, window, scale, out, stream):
     _expect(k, "k", (B, Hkv, Skv, D), dtype)
     _expect(v, "v", (B, Hkv, Skv, D), dtype)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q, stream)
     _expect(out, "out", q.shape, dtype)
     _need_cuda(q, k, v, out)
     if scale is None:
@@ -152,12 +169,10 @@ def attn_prefill_host(q, k, v, *, causal=False, window=0, scale=None, out=None, 
         raise ValueError("out must be a contiguous host tensor")
     _expect(out, "out", q.shape, torch.bfloat16)
     dev = torch.cuda.current_device()
-    own_buffers = device_buffers is None
-    if own_buffers:
-        device_buffers = (torch.empty(q.shape, dtype=torch.bfloat16, device=dev),
-                          torch.empty(k.shape, dtype=torch.bfloat16, device=dev),
-                          torch.empty(v.shape, dtype=torch.bfloat16, device=dev),
-                          torch.empty(q.shape, dtype=torch.bfloat16, device=dev))
+    kernel_stream = torch.cuda.current_stream() if stream is None else stream
+    if device_buffers is None:
+        with torch.cuda.stream(kernel_stream):   # the copy streams start behind it
+            device_buffers = tuple(torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in (q, k, v, q))
     qd, kd, vd, od = device_buffers
     for t, ref, name in ((qd, q, "q_dev"), (kd, k, "k_dev"), (vd, v, "v_dev"), (od, q, "out_dev")):
         _expect(t, name, ref.shape, torch.bfloat16)
@@ -165,13 +180,10 @@ def attn_prefill_host(q, k, v, *, causal=False, window=0, scale=None, out=None, 
     if copy_streams == "auto":
         copy_streams = _copy_streams(dev)
     cin, cout = copy_streams if copy_streams is not None else (None, None)
-    kernel_stream = torch.cuda.current_stream() if stream is None else stream
-    users = [cs for cs in (cin, cout) if cs is not None]
-    if own_buffers and kernel_stream != torch.cuda.current_stream():
-        users.append(kernel_stream)   # allocated on the current stream, used on another
     for t in (qd, kd, vd, od):   # the copy streams use the buffers too: keep them from early reuse
-        for cs in users:
-            t.record_stream(cs)
+        for cs in (cin, cout):
+            if cs is not None:
+                t.record_stream(cs)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     _release_finished_host_calls()
@@ -202,9 +214,9 @@ def _prefill_lse(name, dtype, q, k, v, causal, window, scale, out, lse, stream):
     _expect(k, "k", (B, Hkv, Skv, D), dtype)
     _expect(v, "v", (B, Hkv, Skv, D), dtype)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q, stream)
     if lse is None:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        lse = _new((B, Hq, Sq), torch.float32, q, stream)
     _expect(out, "out", q.shape, dtype)
     _expect(lse, "lse", (B, Hq, Sq), torch.float32)
     _need_cuda(q, k, v, out, lse)
@@ -241,9 +253,9 @@ def attn_prefill_paged(q, k_pool, v_pool, page_table, seq_lens, *, max_seq_len, 
     _expect(page_table, "page_table", (B, max_pages), torch.int32)
     _expect(seq_lens, "seq_lens", (B,), torch.int32)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q, stream)
     if lse is None and want_lse:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        lse = _new((B, Hq, Sq), torch.float32, q, stream)
     _expect(out, "out", q.shape, torch.bfloat16)
     _expect(lse, "lse", (B, Hq, Sq), torch.float32)
     if scale is None:
@@ -283,13 +295,13 @@ def attn_decode_paged(q, k_pool, v_pool, page_table, seq_lens, *, max_seq_len, s
     max_pages = page_table.shape[1]
     _check_decode_args(q, k_pool, v_pool, page_table, seq_lens, torch.bfloat16)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q, stream)
     _expect(out, "out", q.shape, torch.bfloat16)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     need = attn_decode_paged_workspace_size(N, Hq, D, max_seq_len, page_size)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 16), torch.uint8, q, stream, returned=False)
     _need_cuda(q, k_pool, v_pool, page_table, seq_lens, out, workspace)
     if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError("page_table and seq_lens must be int32")
@@ -309,13 +321,13 @@ def attn_decode_paged_fp8(q, k_pool, v_pool, page_table, seq_lens, *, max_seq_le
     max_pages = page_table.shape[1]
     _check_decode_args(q, k_pool, v_pool, page_table, seq_lens, torch.uint8)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q, stream)
     _expect(out, "out", q.shape, torch.bfloat16)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     need = attn_decode_paged_workspace_size(N, Hq, D, max_seq_len, page_size)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 16), torch.uint8, q, stream, returned=False)
     _need_cuda(q, k_pool, v_pool, page_table, seq_lens, out, workspace)
     if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError("page_table and seq_lens must be int32")
@@ -355,12 +367,10 @@ def attn_decode_step_host(q, k_new, v_new, k_pool, v_pool, page_table, seq_lens,
         raise ValueError("out must be a contiguous host tensor")
     _expect(out, "out", q.shape, torch.bfloat16)
     dev = torch.cuda.current_device()
-    own = device_buffers is None
-    if own:
-        device_buffers = (torch.empty(q.shape, dtype=torch.bfloat16, device=dev),
-                          torch.empty(k_new.shape, dtype=torch.bfloat16, device=dev),
-                          torch.empty(v_new.shape, dtype=torch.bfloat16, device=dev),
-                          torch.empty(q.shape, dtype=torch.bfloat16, device=dev))
+    kernel_stream = torch.cuda.current_stream() if stream is None else stream
+    if device_buffers is None:
+        with torch.cuda.stream(kernel_stream):
+            device_buffers = tuple(torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in (q, k_new, v_new, q))
     qd, kd, vd, od = device_buffers
     for t, ref, name in ((qd, q, "q_dev"), (kd, k_new, "k_new_dev"), (vd, v_new, "v_new_dev"), (od, q, "out_dev")):
         _expect(t, name, ref.shape, torch.bfloat16)
@@ -368,12 +378,10 @@ def attn_decode_step_host(q, k_new, v_new, k_pool, v_pool, page_table, seq_lens,
         scale = 1.0 / math.sqrt(D)
     need = attn_decode_paged_workspace_size(N, Hq, D, max_seq_len, page_size)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _new(max(need, 16), torch.uint8, qd, stream, returned=False)
     _need_cuda(qd, kd, vd, od, k_pool, v_pool, page_table, seq_lens, workspace)
-    kernel_stream = torch.cuda.current_stream() if stream is None else stream
     if kernel_stream != torch.cuda.current_stream():
-        for t in ((qd, kd, vd, od) if own else ()) + ((workspace,) if workspace is not None else ()):
-            t.record_stream(kernel_stream)
+        workspace.record_stream(kernel_stream)
     _release_finished_host_calls()
     _check("attn_decode_step_host", _lib.load().attn_decode_step_host(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(out), _ptr(qd), _ptr(kd), _ptr(vd), _ptr(od), _ptr(k_pool),
@@ -398,7 +406,7 @@ def attn_decode_paged_noalloc(q, k_pool, v_pool, page_table, seq_lens, *, max_se
     max_pages = page_table.shape[1]
     _check_decode_args(q, k_pool, v_pool, page_table, seq_lens, torch.bfloat16)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q, stream)
     _expect(out, "out", q.shape, torch.bfloat16)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
@@ -503,23 +511,6 @@ def _on_device(*tensors):
 
 def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _new(shape, dtype, like, stream, returned=True):
-    """A tensor on like's device for a call on `stream` (None: the current stream).
-
-    It is allocated on the stream that writes it: a block of the current stream may still be in use by work
-    queued there, which a call on another stream does not wait for.  One that is returned is likely to be
-    read on the current stream, whose uses up to its release are waited for before its block is used again.
-    """
-    if stream is None or not like.is_cuda:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    here = torch.cuda.current_stream(like.device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=like.device)
-    if returned:
-        t.record_stream(here)
-    return t
 
 
 def _c_int(x):

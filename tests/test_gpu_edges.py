@@ -45,3 +45,42 @@ def test_append_of_nothing_is_a_no_op():
     api.attn_kv_append(k_new, k_new, kp, kp, table, lens)
     torch.cuda.synchronize()
     assert torch.equal(kp, before)
+
+
+def test_calls_on_another_stream_are_not_overwritten_by_work_queued_on_this_one():
+    """The current stream still has to fill blocks that were released on the host: no result or scratch of a
+    call on another stream may lie in them."""
+    inp = inputs.prefill_inputs(1, 8, 2, 500, 500, 64, seed=4)
+    q, k, v = inp.q.cuda(), inp.k.cuda(), inp.v.cuda()
+    host = [x.pin_memory() for x in (inp.q, inp.k, inp.v)]
+    p = inputs.paged_inputs(3, 8, 2, 64, 16, seed=6, seq_lens=[1500, 900, 77])
+    dq, kp, vp, pt, sl = (x.cuda() for x in (p.q, p.k_pool, p.v_pool, p.page_table, p.seq_lens))
+    new = [x.pin_memory() for x in (p.q, inputs.normal((3, 2, 1, 64), 8), inputs.normal((3, 2, 1, 64), 9))]
+
+    def calls(**kw):
+        return [api.attn_prefill(q, k, v, causal=True, **kw), *api.attn_prefill_lse(q, k, v, **kw),
+                api.attn_prefill_f32(q.float(), k.float(), v.float(), **kw),
+                api.attn_decode_paged(dq, kp, vp, pt, sl, max_seq_len=1500, **kw),
+                api.attn_prefill_host(*host, causal=True, **kw),
+                api.attn_decode_step_host(*new, kp, vp, pt, sl, max_seq_len=1500, **kw)]
+
+    calls()                                    # (the step appends its token: the same one below)
+    want = calls()
+    need = api.attn_decode_paged_workspace_size(3, 8, 64, 1500, 16)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    s.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(200_000_000)             # some 100 ms
+    for _ in range(3):
+        for size in (2 * q.numel(), 4 * q.numel(), 2 * k.numel(), 8 * 500 * 4, 2 * dq.numel(), 2 * new[1].numel(), need):
+            torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    with torch.cuda.stream(s):
+        f32 = [x.float() for x in (q, k, v)]
+    got = [api.attn_prefill(q, k, v, causal=True, stream=s), *api.attn_prefill_lse(q, k, v, stream=s),
+           api.attn_prefill_f32(*f32, stream=s), api.attn_decode_paged(dq, kp, vp, pt, sl, max_seq_len=1500, stream=s),
+           api.attn_prefill_host(*host, causal=True, stream=s),
+           api.attn_decode_step_host(*new, kp, vp, pt, sl, max_seq_len=1500, stream=s)]
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 0
+    for i, (g, w) in enumerate(zip(got, want)):
+        assert torch.equal(g, w), i

@@ -298,3 +298,26 @@ def test_what_a_packed_call_allocates_comes_from_its_stream(streams):
     for kw in (dict(out=t(600, 8, 64), lse=t(600, 8, dtype=torch.float32), workspace=t(4096), stream=stream), {}):
         api.attn_prefill_packed(q, k, k, i32(2), **kw)
     assert made == ["current"] * 2 and not recorded           # without a stream: out and workspace on the current one
+
+
+def test_what_the_other_calls_allocate_comes_from_their_stream(streams, monkeypatch):
+    stream, made, recorded = streams
+    monkeypatch.setattr(api, "_need_cuda", lambda *ts: None)
+    q4, k4 = on_card(t(1, 8, 600, 64)), on_card(t(1, 2, 600, 64))
+    q, pool, table, lens = on_card(t(1, 8, 64)), on_card(t(40, 2, 16, 64)), i32(1, 40), i32(1)
+    codes = on_card(t(40, 2, 16, 64, dtype=torch.uint8))
+    out4, lse4, out = ((1, 8, 600, 64), "current"), ((1, 8, 600), "current"), ((1, 8, 64), "current")
+    f32 = [on_card(x.float()) for x in (q4, k4, k4)]
+    for fn, args, kw, n, returned in [
+            (api.attn_prefill, (q4, k4, k4), {}, 1, [out4]),
+            (api.attn_prefill_lse, (q4, k4, k4), {}, 2, [out4, lse4]),
+            (api.attn_prefill_f32, f32, {}, 1, [out4]),
+            (api.attn_prefill_f32_lse, f32, {}, 2, [out4, lse4]),
+            (api.attn_prefill_paged, (q4, pool, pool, table, lens), dict(max_seq_len=640, want_lse=True), 2, [out4, lse4]),
+            (api.attn_decode_paged, (q, pool, pool, table, lens), dict(max_seq_len=640), 2, [out]),
+            (api.attn_decode_paged_noalloc, (q, pool, pool, table, lens), dict(max_seq_len=640), 1, [out]),
+            (api.attn_decode_paged_fp8, (q, codes, codes, table, lens), dict(max_seq_len=640, k_scale=1, v_scale=1), 2,
+             [out])]:
+        fn(*args, stream=stream, **kw)
+        assert made == [stream] * n and recorded == returned, fn.__name__
+        del made[:], recorded[:]
