@@ -5,8 +5,11 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-// Upper bound of any single device-side wait (1 s).  No legitimate wait in
-// these kernels lasts more than a few microseconds.
+// Upper bound of any single device-side wait (1 s).  No legitimate wait of the
+// dense prefill and the decode lasts more than a few microseconds.  In the
+// packed prefill some roles wait while others work through a whole item, as
+// long as its keys make it: there the bound is on the time in which no key tile
+// and no item is taken up, and 8 times as long for the waits within a tile.
 #ifndef ATTN_WAIT_NS
 #define ATTN_WAIT_NS 1000000000ull
 #endif

@@ -202,6 +202,13 @@ __device__ __forceinline__ int block_of(const PackedSteps& l, int causal, int q,
   return min((q + 1) << shift, l.o + l.nb) - 1 - l.o - j;
 }
 
+// A wait for another role's part in a tile (the others are renewed by progress).  Microseconds; but the last V of
+// an item comes once the scheduler knows the next item, and it may have many without keys to pass over:
+// some half a second of 65535 sequences with 1024 kv heads.
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* err) {
+  return mbar_wait_for(bar, parity, abort, err, 8 * ATTN_WAIT_NS);
+}
+
 // The key-tile ranges of an item's query tiles: those that hold a key some row sees.
 __device__ __forceinline__ void packed_ranges(const Params& p, Item& it) {
   const int off = it.sk - it.sq;
@@ -302,9 +309,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   uint64_t* tail_go = item_empty + kItemRing;           // 1: a V tile with rows to zero has landed
   uint64_t* tail_done = tail_go + 1;                    // 1: they are zero
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail_done + 1);
+  // and behind it the counts that renew the waits (wait_is_over): stages filled, items of a pass looked at
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Item* item_ring = reinterpret_cast<Item*>(tmem_slot + 2);   // kItemRing
-  static_assert((2 * QBUF + 2 * STAGES + 4 * NQ + 3 + 2 * kItemRing) * 8 + 8 + kItemRing * sizeof(Item) <= C::CONTROL,
+  Item* item_ring = reinterpret_cast<Item*>(tmem_slot + 4);   // kItemRing
+  static_assert((2 * QBUF + 2 * STAGES + 4 * NQ + 3 + 2 * kItemRing) * 8 + 16 + kItemRing * sizeof(Item) <= C::CONTROL,
                 "barriers and item ring");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     }
     mbar_init(tail_go, 1);
     mbar_init(tail_done, 32);
-    *abort_flag = 0;
+    abort_flag[0] = abort_flag[1] = abort_flag[2] = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   // gave up.  whole_warp: all 32 lanes call (one lane arrives for them).
   auto next_item = [&](int r, bool whole_warp, Item& it) -> bool {
     const int slot = r % kItemRing;
-    bool got = mbar_wait(&item_full[slot], (r / kItemRing) & 1, abort_flag, p.err);
+    bool got = mbar_wait<true>(&item_full[slot], (r / kItemRing) & 1, abort_flag, p.err);
     if (whole_warp) got = __all_sync(0xffffffffu, got);
     it.b = -1;
     if (!got) return false;
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       bool ok = true;
       auto load_q = [&](const Item& it) -> bool {
         const int qb = qn % QBUF;
-        if (qn >= QBUF && !uni(mbar_wait(&q_empty[qb], ((qn / QBUF) - 1) & 1, abort_flag, p.err))) return false;
+        if (qn >= QBUF && !uni(mbar_wait<true>(&q_empty[qb], ((qn / QBUF) - 1) & 1, abort_flag, p.err))) return false;
         if (lead) {
           // a tile without tokens is not loaded; nothing multiplies it either
           const int nt = (it.row0 + tpt < it.end) ? NQ : 1;
@@ -446,13 +454,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // next stage <- V of tile vj of v (unless null), then K of tile kj of k (unless null)
       auto load_stage = [&](const Item* v, int vj, int vph, const Item* k, int kj, int kph) -> bool {
         const int st = n % STAGES;
-        if (!uni(mbar_wait(&empty[st], ((n / STAGES) & 1) ^ 1, abort_flag, p.err))) return false;
+        if (!uni(mbar_wait<true>(&empty[st], ((n / STAGES) & 1) ^ 1, abort_flag, p.err))) return false;
         if (lead) mbar_arrive_expect_tx(&full[st], (v ? C::TILE_BYTES : 0) + (k ? C::TILE_BYTES : 0));
         if constexpr (PAGED) __syncwarp();   // the barrier is armed before any box can land
         uint8_t* dst = sRing + st * C::STAGE_BYTES;
         if (v) copy_tile(dst, &tmap_v, &full[st], *v, vj, vph);
         if (k) copy_tile(dst + (C::SEP_P ? 0 : C::TILE_BYTES), &tmap_k, &full[st], *k, kj, kph);
         ++n;
+        if (lead) abort_flag[1] = n;
         return true;
       };
       Item it;
@@ -540,13 +549,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           mma_ts(o_tmem, p_tmem + kk * 8, desc64(b_lo + ((kk * 16 * 128) >> 4), kHi), idesc_pv, kk > 0 ? 1u : acc0);
       };
       auto wait_p = [&](int i) -> bool {
-        const bool got = mbar_wait(&p_ready[i], (tp >> i) & 1, abort_flag, p.err);
+        const bool got = tile_wait(&p_ready[i], (tp >> i) & 1, abort_flag, p.err);
         tp ^= 1u << i;
         tc_fence_after();
         return got;
       };
       auto wait_stage = [&](int st) -> bool {
-        const bool got = mbar_wait(&full[st], (n / STAGES) & 1, abort_flag, p.err);
+        const bool got = tile_wait(&full[st], (n / STAGES) & 1, abort_flag, p.err);
         tc_fence_after();
         return got;
       };
@@ -559,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         return true;
       };
       auto tail_wait = [&]() -> bool {
-        const bool got = mbar_wait(tail_done, tails & 1, abort_flag, p.err);
+        const bool got = tile_wait(tail_done, tails & 1, abort_flag, p.err);
         ++tails;
         return got;
       };
@@ -572,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         uint32_t used = 0, tf = 0;   // bit i: S_i was written before; parity of s_free's next phase
         auto issue_next_s = [&](int i, int qb, int st) -> bool {
           if (used & (1u << i)) {
-            if (!mbar_wait(&s_free[i], (tf >> i) & 1, abort_flag, p.err)) return false;
+            if (!tile_wait(&s_free[i], (tf >> i) & 1, abort_flag, p.err)) return false;
             tf ^= 1u << i;
             tc_fence_after();
           }
@@ -582,7 +591,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         };
         while (have && ok) {
           const int qb = qn % QBUF;
-          if (!(ok = mbar_wait(&q_full[qb], (qn / QBUF) & 1, abort_flag, p.err))) break;
+          if (!(ok = tile_wait(&q_full[qb], (qn / QBUF) & 1, abort_flag, p.err))) break;
           tc_fence_after();
           ++qn;
           int st = n % STAGES;
@@ -633,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (have) ok = wait_stage(0);
         while (have && ok) {
           const int qb = qn % QBUF;
-          if (!(ok = mbar_wait(&q_full[qb], (qn / QBUF) & 1, abort_flag, p.err))) break;
+          if (!(ok = tile_wait(&q_full[qb], (qn / QBUF) & 1, abort_flag, p.err))) break;
           tc_fence_after();
           ++qn;
           int st = n % STAGES;   // holds the V of the tile before (used up) and this item's first K
@@ -732,6 +741,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       for (int r = 0;; ++r) {
         const int P = gridDim.x, c = blockIdx.x;
         const int k = r * P + ((r & 1) ? (P - 1 - c) : c);
+        if (lane == 0) abort_flag[2] = r;
         const int unit = SPLIT ? k / p.splits : k;
         const int rank = unit / p.head_blocks;
         while (level >= 0 && rank >= base + count) {
@@ -798,7 +808,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (it.b < 0 && none && !rows_left) break;   // the second pass ends the list
         const int slot = put % kItemRing;
         if (!__all_sync(0xffffffffu,
-                        mbar_wait_idle(&item_empty[slot], ((put / kItemRing) & 1) ^ 1, abort_flag, p.err))) {
+                        mbar_wait_idle<true>(&item_empty[slot], ((put / kItemRing) & 1) ^ 1, abort_flag, p.err))) {
           go_on = false;
           break;
         }
@@ -815,7 +825,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     int tiles = 0, tails = 0;   // key tiles of the items so far, V tiles zeroed
     for (int r = 0;; ++r) {
       Item it;
-      if (!__all_sync(0xffffffffu, mbar_wait_idle(&item_full[r % kItemRing], (r / kItemRing) & 1, abort_flag, p.err)))
+      if (!__all_sync(0xffffffffu, mbar_wait_idle<true>(&item_full[r % kItemRing], (r / kItemRing) & 1, abort_flag, p.err)))
         break;
       if (!next_item(r, true, it)) break;
       tiles += it.hi_all - it.lo_all;
@@ -825,8 +835,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (to <= from) continue;
       const int st = n % STAGES;
       // the MMA thread has seen the stage land, and frees it only after tail_done
-      bool got = mbar_wait_idle(tail_go, tails & 1, abort_flag, p.err);
-      got = got && mbar_wait(&full[st], (n / STAGES) & 1, abort_flag, p.err);
+      bool got = mbar_wait_idle<true>(tail_go, tails & 1, abort_flag, p.err);
+      got = got && mbar_wait<true>(&full[st], (n / STAGES) & 1, abort_flag, p.err);
       if (!__all_sync(0xffffffffu, got)) break;
       ++tails;
       for (int a = 0; a < C::KATOMS; ++a) {
@@ -903,7 +913,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       float m_ref = -INFINITY, l = 0.f;
 
       for (int j = my_lo; j < my_hi; ++j, ++t) {
-        ok = mbar_wait(&s_ready[i], t & 1, abort_flag, p.err);
+        ok = tile_wait(&s_ready[i], t & 1, abort_flag, p.err);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
@@ -964,7 +974,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         // P_i is rewritten.  Waiting here hides that product behind them.
         if constexpr (C::SEP_P) {
           if (j > my_lo) {
-            ok = mbar_wait(&o_done[i], pv & 1, abort_flag, p.err);
+            ok = tile_wait(&o_done[i], pv & 1, abort_flag, p.err);
             ++pv;
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
@@ -983,10 +993,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (!ok) break;
       // ---- epilogue: O / l -> bf16 (tcgen05.ld is warp-collective: every lane loads)
       if constexpr (C::SEP_P) {
-        ok = mbar_wait(&o_done[i], pv & 1, abort_flag, p.err);
+        ok = tile_wait(&o_done[i], pv & 1, abort_flag, p.err);
         ++pv;
       } else {
-        ok = mbar_wait(&o_done[i], oc & 1, abort_flag, p.err);
+        ok = tile_wait(&o_done[i], oc & 1, abort_flag, p.err);
         ++oc;
       }
       if (!__all_sync(0xffffffffu, ok)) {

@@ -67,18 +67,40 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// True if a wait that began or was renewed at t0 has lasted limit_ns.  PROGRESS: without progress.
+// abort[1] and abort[2] are then two counts, each kept by one role, that move as long as the kernel goes
+// on; if they have since the last look, the wait is renewed.  The first look always renews it, so a
+// wait for a role that stands still lasts up to twice the limit.
+template <bool PROGRESS>
+__device__ __forceinline__ bool wait_is_over(uint64_t& t0, uint64_t limit_ns, volatile int* abort, int& seen) {
+  const uint64_t now = globaltimer_ns();
+  if (now - t0 <= limit_ns) return false;
+  if constexpr (PROGRESS) {
+    const int sum = (abort[1] + abort[2]) & 0x7FFFFFFF;   // (never the -1 that seen begins with)
+    if (sum != seen) {
+      seen = sum;
+      t0 = now;
+      return false;
+    }
+  }
+  return true;
+}
+
 // Wait until the phase of `bar` with parity `parity` has completed.  Gives up
-// after limit_ns, or at once if *abort is already set; returns false then,
-// having recorded ATTN_ERRBIT_TIMEOUT and set *abort for the other roles.
+// after limit_ns (PROGRESS: as above), or at once if *abort is already set;
+// returns false then, having recorded ATTN_ERRBIT_TIMEOUT and set *abort for
+// the other roles.
+template <bool PROGRESS = false>
 __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, volatile int* abort,
                                               unsigned int* err, uint64_t limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = globaltimer_ns();
+  int seen = -1;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 255u) == 0u) {
       if (abort != nullptr && *abort) return false;
-      if (globaltimer_ns() - t0 > limit_ns) {
+      if (wait_is_over<PROGRESS>(t0, limit_ns, abort, seen)) {
         record_error(err, ATTN_ERRBIT_TIMEOUT);
         if (abort != nullptr) *abort = 1;
         return false;
@@ -88,20 +110,23 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, vo
 }
 
 // mbar_wait_for with the library's limit, ATTN_WAIT_NS.
+template <bool PROGRESS = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           unsigned int* err) {
-  return mbar_wait_for(bar, parity, abort, err, ATTN_WAIT_NS);
+  return mbar_wait_for<PROGRESS>(bar, parity, abort, err, ATTN_WAIT_NS);
 }
 
 // mbar_wait for a role that has long waits and no haste: it sleeps between
 // polls, so that it takes no issue slots from the warps that work.
+template <bool PROGRESS = false>
 __device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                unsigned int* err) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
+  uint64_t t0 = globaltimer_ns();
+  int seen = -1;
   while (!mbar_try_wait(bar, parity)) {
     if (abort != nullptr && *abort) return false;
-    if (globaltimer_ns() - t0 > ATTN_WAIT_NS) {
+    if (wait_is_over<PROGRESS>(t0, ATTN_WAIT_NS, abort, seen)) {
       record_error(err, ATTN_ERRBIT_TIMEOUT);
       if (abort != nullptr) *abort = 1;
       return false;

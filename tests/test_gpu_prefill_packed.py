@@ -508,3 +508,40 @@ def test_a_call_on_another_stream_is_not_overwritten_by_work_queued_on_this_one(
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(again, turned)
     assert api.attn_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_item_may_last_longer_than_any_wait_is_allowed_to(D):
+    """One row over 2^28 keys on one SM, some 3 s: the roles that wait for the end of the item go on waiting as long as
+    key tiles pass (a wait without progress ends after 2 s).
+
+    The page table names page 0 over and over, with scores of 0 and v that alternates in sign, and page 1
+    at the end, whose 156 keys weigh e^28 or more each: the result is the mean of their v, which is made of
+    eighths (at most 2^-12 of its weight goes to page 0, whose v cancel).  The weights are within 2^-17
+    of equal (the fp32 score of at most 58, in log2 units, against the row's maximum)."""
+    import ctypes
+
+    from scaled_dot_product_prefill_b200 import _lib
+
+    L, page = 2 ** 28 - 100, 256
+    kp, vp = (torch.zeros((2, 1, page, D), dtype=torch.bfloat16) for _ in range(2))
+    kp[1], q = 3.5, torch.ones((1, 1, D), dtype=torch.bfloat16)
+    vp[0, 0, ::2], vp[0, 0, 1::2] = 1.0, -1.0
+    vp[1, 0] = torch.from_numpy(np.random.default_rng(D).integers(0, 9, (page, D)) / 8).to(torch.bfloat16)
+    table = torch.zeros((1, -(-L // page)), dtype=torch.int32)
+    table[0, -1] = 1
+    lens, cu = torch.tensor([L], dtype=torch.int32).cuda(), cumulative([1]).cuda()
+    dev = [x.cuda() for x in (q, kp, vp, table)]
+    out, lse = torch.full((1, 1, D), 9.0, dtype=torch.bfloat16, device="cuda"), torch.full((1, 1), 7.0, device="cuda")
+    api.attn_device_status(clear=True)
+    st = _lib.load().attn_prefill_packed_paged(
+        dev[0].data_ptr(), dev[1].data_ptr(), dev[2].data_ptr(), cu.data_ptr(), dev[3].data_ptr(), lens.data_ptr(), page, 1,
+        1, 1, 1, D, D, D, 2, table.shape[1], L, D ** -0.5, 1, 0, None, 0, out.data_ptr(), lse.data_ptr(),
+        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert st == 0 and api.attn_device_status(clear=True) == 0
+    n, w = L % page, np.exp(3.5 * D ** 0.5)
+    want = f64(vp[1, 0, :n]).sum(0) * w / (n * w + (L - n))
+    assert (np.abs(f64(out)[0, 0] - want) <= (2.0 ** -8 + 2.0 ** -16) * want).all()
+    want = np.log(n * w + (L - n))
+    assert abs(float(lse) - want) <= 2.0 ** -17 + 2.0 ** -22 * (want + 16)
