@@ -545,3 +545,95 @@ def test_an_item_may_last_longer_than_any_wait_is_allowed_to(D):
     assert (np.abs(f64(out)[0, 0] - want) <= (2.0 ** -8 + 2.0 ** -16) * want).all()
     want = np.log(n * w + (L - n))
     assert abs(float(lse) - want) <= 2.0 ** -17 + 2.0 ** -22 * (want + 16)
+
+
+def repeated_pages(q, kp, vp, L, workspace=False):
+    """(out, lse) of one sequence of L keys whose page table names the pool's pages over and over, on one SM (without a
+    workspace) or split; q [1, 1, D]."""
+    import ctypes
+
+    from scaled_dot_product_prefill_b200 import _lib
+
+    num, _, page, D = kp.shape
+    table = (torch.arange(-(-L // page), dtype=torch.int32) % num).view(1, -1).cuda()
+    lens, cu = torch.tensor([L], dtype=torch.int32).cuda(), cumulative([1]).cuda()
+    q, kp, vp = q.cuda(), kp.cuda(), vp.cuda()
+    need = api.attn_prefill_packed_workspace_size(1, 1, 1, 1, D, L) if workspace else 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(q, 9.0), torch.full((1, 1), 7.0, device="cuda")
+    api.attn_device_status(clear=True)
+    st = _lib.load().attn_prefill_packed_paged(
+        q.data_ptr(), kp.data_ptr(), vp.data_ptr(), cu.data_ptr(), table.data_ptr(), lens.data_ptr(), page, 1, 1, 1, 1, D, D,
+        D, num, table.shape[1], L, D ** -0.5, 1, 0, ws.data_ptr() if workspace else None, need, out.data_ptr(),
+        lse.data_ptr(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert st == 0 and api.attn_device_status(clear=True) == 0
+    return f64(out)[0, 0], float(lse)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_sum_over_many_keys_of_like_weight(D):
+    """2^28 keys of equal weight, v 0, 1 or 2 of one sign a column.  A run of 2^16 keys sums to 2^16 v, the runs to
+    multiples of that below 2^29: exact in fp32.  The last, shorter run and the sum of the weights round by
+    2^-24 each, which no bf16 value of 0, 1 or 2 notices."""
+    L = 2 ** 28 - 100
+    v = (torch.arange(D) % 5 - 2).to(torch.bfloat16)
+    out, lse = repeated_pages(torch.zeros((1, 1, D), dtype=torch.bfloat16), inputs.normal((1, 1, 256, D), 1),
+                              v.expand(1, 1, 256, D).contiguous(), L)
+    assert np.array_equal(out, f64(v))
+    assert abs(lse - np.log(L)) <= 2.0 ** -22 * (np.log(L) + 16)
+
+
+@pytest.mark.parametrize("D,log2_keys,workspace", [(64, 18, False), (64, 19, False), (64, 22, False), (128, 20, False),
+                                                   (128, 22, False), (64, 22, True), (64, 24, True), (128, 24, True)])
+def test_values_of_one_sign_lose_nothing_to_the_length(D, log2_keys, workspace):
+    """Equal weights (of exactly 1), v in [0, 1): the mean of v.
+
+    The tensor core aligns 16 products with their sum and drops what lies below 2^-25 of it (as measured: a
+    product of 1 is lost beside 2^26, not beside 2^25), and its result is an fp32 value.  A run of 2^16 keys so
+    loses 2^16 2^-25 of itself and 2^12 2^-23 at most; up to 2^18 keys (here: the part of a split too) are
+    one run.  The up to 2^8 runs round by 2^-24 each, the output by 2^-8.  (One run over all keys lost
+    2.2 % of 2^22, 35 % of 2^26.)"""
+    r = np.random.default_rng(D + log2_keys)
+    vp = torch.from_numpy(r.random((64, 1, 256, D))).to(torch.bfloat16)
+    out, lse = repeated_pages(torch.zeros((1, 1, D), dtype=torch.bfloat16), inputs.normal((64, 1, 256, D), 1), vp,
+                              2 ** log2_keys, workspace)
+    want = f64(vp).reshape(-1, D).mean(0)
+    part = log2_keys - 4 * workspace
+    run = 2.0 ** (part if part <= 18 else 16)
+    assert (np.abs(out - want) <= (run * (2.0 ** -25 + 2.0 ** -27) + 2.0 ** -16 + 2.0 ** -8) * want).all()
+    want = log2_keys * np.log(2)
+    assert abs(lse - want) <= 2.0 ** -22 * (want + 16)
+
+
+@pytest.mark.parametrize("D,causal,window", [(64, True, 0), (128, True, 0), (64, False, 0), (128, True, 280_000),
+                                             (64, True, 66_000)])
+def test_runs_of_keys_are_joined(D, causal, window):
+    """Rows over two and more runs of 2^16 keys (one run, with the shortest window), with scores whose maximum grows along the keys (and, in the
+    third head, falls), without a workspace."""
+    import ctypes
+
+    from scaled_dot_product_prefill_b200 import _lib
+
+    Hq, Hkv, lk = 4, 2, [300_000, 130_000]      # (more than 2^18 rows in the buffer)
+    cu_q, cu_k = cumulative([3, 200]), cumulative(lk)
+    q, k, v = tensors(203, sum(lk), Hq, Hkv, D, 3)
+    ramp = torch.cat([torch.arange(n) / n for n in lk])[:, None, None]
+    k = (k.float() * torch.cat((0.2 + 2 * ramp, 2 - 1.9 * ramp), 1)).to(torch.bfloat16)
+    v = (v.float() + 0.5).to(torch.bfloat16)
+    dev = [x.cuda() for x in (q, k, v, cu_q, cu_k)]
+    out, lse = torch.empty_like(dev[0]), torch.empty((203, Hq), device="cuda")
+    api.attn_device_status(clear=True)
+    st = _lib.load().attn_prefill_packed(
+        *(x.data_ptr() for x in dev), 2, 203, sum(lk), Hq, Hkv, D, Hq * D, Hkv * D, Hkv * D, Hq * D, D ** -0.5, int(causal),
+        window, None, 0, out.data_ptr(), lse.data_ptr(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert st == 0 and api.attn_device_status(clear=True) == 0
+    some = [0, 1, 2, 3, 66, 135, 202]           # rows that the definition is evaluated at
+    for b, (a, e) in enumerate(zip(cu_k.tolist(), cu_k.tolist()[1:])):
+        for i in [x for x in some if cu_q[b] <= x < cu_q[b + 1]]:
+            last = e - (int(cu_q[b + 1]) - 1 - i) if causal else e
+            first = max(a, last - window) if window else a
+            want = packed_attention(f64(q[i:i + 1]), f64(k[first:last]), f64(v[first:last]), [0, 1], [0, last - first],
+                                    D ** -0.5)
+            assert_packed((out[i:i + 1], lse[i:i + 1]), want, f"row {i}")
