@@ -306,8 +306,8 @@ attn_status_t attn_prefill_packed(const void* q, const void* k, const void* v,
 
 /* Bytes of workspace with which attn_prefill_packed_paged, and attn_prefill_packed
  * (max_seq_len: Tk / B rounded up, as if its sequences were equally long), split
- * long sequences; 0 for sizes that are not split, or invalid.  Pure host
- * arithmetic, no CUDA call. */
+ * long sequences; 0 for sizes that are not split, or invalid.  With a window a
+ * call may use less of it, or none.  Pure host arithmetic, no CUDA call. */
 size_t attn_prefill_packed_workspace_size(int B, int Tq, int Hq, int Hkv, int D, int max_seq_len);
 
 /*

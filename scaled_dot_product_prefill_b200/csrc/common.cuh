@@ -81,7 +81,7 @@ cudaError_t launch_prefill_tc_paged(const void* q, const void* k_pool, const voi
 // Packed sequences: q/out [Tq, Hq, D], k/v [Tk, Hkv, D] with token strides in elements, cumulative
 // lengths cu_q, cu_k [B + 1] on the device; lse (optional) [Tq, Hq].  The workspace (optional, of
 // packed_workspace_bytes) lets the key tiles of few items be dealt to packed_splits parts each.
-int packed_splits(int B, int Tq, int Hq, int Hkv, int max_seq_len);
+int packed_splits(int B, int Tq, int Hq, int Hkv, int max_seq_len, int window);
 inline int keys_each(int Tk, int B) { return B > 0 ? static_cast<int>((static_cast<long long>(Tk) + B - 1) / B) : 0; }
 size_t packed_workspace_bytes(int B, int Tq, int Hq, int Hkv, int D, int max_seq_len);
 cudaError_t launch_prefill_tc_packed(const void* q, const void* k, const void* v, const int32_t* cu_q,

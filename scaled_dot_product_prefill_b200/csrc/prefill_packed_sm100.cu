@@ -1302,24 +1302,33 @@ long long item_bound(int B, int Tq, int Hq, int Hkv) {
 // the tiles mostly empty (few rows) a part may be a single key tile: 600 keys took 15.9 us whole
 // and 12.3 in 5.  With full tiles the parts' rows cost as much to write and join as 4 key
 // tiles: a 512-token prompt, 12 heads, took 13.5 us whole and 17.2 in 2, 1024 tokens 20.6 and 19.4.
-int packed_splits(int B, int Tq, int Hq, int Hkv, int max_seq_len) {
+// With a window (causal) an item has no more parts than key tiles that it sees, and is whole if they are 3: 2
+// sequences x 9 tokens over 8192 keys, 8/2 heads, took 12.1 us whole and 12.6 in 16 parts with a window
+// of 128, 9.4 and 12.1 with one of 32; 15.0 and 12.8 with one of 256, 4 key tiles.
+int packed_splits(int B, int Tq, int Hq, int Hkv, int max_seq_len, int window) {
   if (B <= 0 || Tq <= 0 || Hq <= 0 || Hkv <= 0) return 1;
   const int s = pack_log2_of(Hq, Hkv);
   const int block = (BM >> s) * NQ;
   const long long each = (static_cast<long long>(Tq) + B - 1) / B;
   const long long items = (each + block - 1) / block * B * (Hq >> s);
   const int tiles = (max_seq_len + BN - 1) / BN;
-  if (tiles < 4) return 1;
+  long long seen = tiles;
+  if (window > 0) {   // n tokens see window + n - 1 keys in a row: the tiles that those may touch
+    const long long keys = window + (each < block ? each : block) - 1;
+    if ((keys + BN - 2) / BN + 1 < seen) seen = (keys + BN - 2) / BN + 1;
+  }
+  if (seen < 4) return 1;
   const bool few_rows = static_cast<long long>(Tq) * Hq <= items * (NQ * BM / 4);
   long long parts = 148 / items;
   const int most = few_rows ? tiles : tiles / 4;
   if (parts > most) parts = most;
+  if (parts > seen) parts = seen;
   if (parts > 16) parts = 16;
   return parts < 2 ? 1 : static_cast<int>(parts);
 }
 
 size_t packed_workspace_bytes(int B, int Tq, int Hq, int Hkv, int D, int max_seq_len) {
-  const int s = packed_splits(B, Tq, Hq, Hkv, max_seq_len);
+  const int s = packed_splits(B, Tq, Hq, Hkv, max_seq_len, 0);   // (a window never means more parts)
   return s < 2 ? 0 : static_cast<size_t>(s) * Tq * Hq * (D + 1) * sizeof(float);
 }
 
@@ -1345,7 +1354,7 @@ bool packed_params(Params& p, void* out, float* lse, const int32_t* cu_q, int B,
   p.pack_log2 = pack_log2_of(Hq, Hkv);
   p.head_blocks = Hq >> p.pack_log2;
   // the caller's workspace decides whether an item is split (none: never)
-  p.splits = workspace != nullptr ? packed_splits(B, Tq, Hq, Hkv, max_seq_len) : 1;
+  p.splits = workspace != nullptr ? packed_splits(B, Tq, Hq, Hkv, max_seq_len, window) : 1;
   p.ws_o = static_cast<float*>(workspace);
   if (p.splits > 1) p.ws_lse = p.ws_o + static_cast<size_t>(p.splits) * Tq * Hq * D;
   // items are counted in int32, with room for one more round of the grid

@@ -637,3 +637,33 @@ def test_runs_of_keys_are_joined(D, causal, window):
             want = packed_attention(f64(q[i:i + 1]), f64(k[first:last]), f64(v[first:last]), [0, 1], [0, last - first],
                                     D ** -0.5)
             assert_packed((out[i:i + 1], lse[i:i + 1]), want, f"row {i}")
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,new,window,split", [
+    (8, 2, 128, 16, [9, 9], 1, False), (8, 2, 128, 16, [9, 9], 128, False), (8, 2, 128, 16, [9, 9], 256, True),
+    (8, 2, 128, 0, [9, 9], 128, False), (8, 2, 128, 0, [9, 9], 1000, True), (16, 16, 64, 32, [1], 256, False),
+    (16, 16, 64, 32, [1], 400, True), (4, 4, 64, 0, [200, 100], 100, False), (8, 2, 128, 64, [9, 9], 2 ** 31 - 1, True)])
+def test_only_key_tiles_in_the_window_are_worth_a_split(Hq, Hkv, D, page, new, window, split):
+    """Rows that see 3 key tiles at most through their window are not split over a long cache; the workspace shows it."""
+    lk = [4000 + 100 * b for b in range(len(new))]
+    cu_q, cu_k = cumulative(new), cumulative(lk)
+    q = inputs.normal((sum(new), Hq, D), 5)
+    need = api.attn_prefill_packed_workspace_size(len(new), sum(new), Hq, Hkv, D, max(lk))
+    assert need > 0
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device="cuda")
+    api.attn_device_status(clear=True)
+    if page:
+        p = inputs.paged_inputs(len(lk), Hq, Hkv, D, page, seed=9, seq_lens=lk, spare_pages=3, poison=True)
+        K, V = gathered(p, lk)
+        got = api.attn_prefill_packed_paged(q.cuda(), p.k_pool.cuda(), p.v_pool.cuda(), cu_q.cuda(), p.page_table.cuda(),
+                                            p.seq_lens.cuda(), max_seq_len=max(lk), window=window, want_lse=True,
+                                            workspace=ws)
+    else:
+        k, v = inputs.normal((sum(lk), Hkv, D), 6), inputs.normal((sum(lk), Hkv, D), 7)
+        K, V = f64(k), f64(v)
+        got = api.attn_prefill_packed(q.cuda(), k.cuda(), v.cuda(), cu_q.cuda(), cu_k.cuda(), window=window,
+                                      want_lse=True, workspace=ws)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 0
+    assert bool((ws != 0xA5).any()) == split
+    assert_packed(got, packed_attention(f64(q), K, V, cu_q.tolist(), cu_k.tolist(), D ** -0.5, True, window))
