@@ -542,8 +542,7 @@ def _packed_results(q, Tq, Hq, D, out, lse, want_lse, stream):
 
 
 def attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, max_seq_len) -> int:
-    return int(_lib.load().attn_prefill_packed_workspace_size(int(B), int(Tq), int(Hq), int(Hkv), int(D),
-                                                              int(max_seq_len)))
+    return int(_lib.load().attn_prefill_packed_workspace_size(*map(_c_int, (B, Tq, Hq, Hkv, D, max_seq_len))))
 
 
 def _packed_workspace(workspace, B, Tq, Hq, Hkv, D, max_seq_len, q, stream):

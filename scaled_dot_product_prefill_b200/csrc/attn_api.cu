@@ -225,7 +225,7 @@ int cut_window(int window) { return window < (1 << 30) ? window : (1 << 30); }
 }  // namespace
 
 size_t attn_prefill_packed_workspace_size(int B, int Tq, int Hq, int Hkv, int D, int max_seq_len) {
-  if (B <= 0 || Tq <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || D <= 0 || max_seq_len < 0) return 0;
+  if (B <= 0 || Tq <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128) || max_seq_len < 0) return 0;
   if (B > 65535 || Tq > (1 << 30) || max_seq_len > (1 << 30)) return 0;   // sizes that the calls refuse
   return attn::packed_workspace_bytes(B, Tq, Hq, Hkv, D, max_seq_len);
 }

@@ -321,3 +321,21 @@ def test_what_the_other_calls_allocate_comes_from_their_stream(streams, monkeypa
         fn(*args, stream=stream, **kw)
         assert made == [stream] * n and recorded == returned, fn.__name__
         del made[:], recorded[:]
+
+
+def test_the_workspace_size_of_a_head_dim_or_a_number_that_no_call_takes_is_none():
+    size = api.attn_prefill_packed_workspace_size
+    good = (2, 10, 8, 2, 128, 8192)
+    assert size(*good) > 0
+    for D in (32, 96, 256, 2 ** 31 - 1):
+        assert size(2, 10, 8, 2, D, 8192) == 0
+    for i in range(6):                          # beyond a C int: not what its low 32 bits say
+        for far in (2 ** 32, -2 ** 32, 2 ** 40):
+            assert size(*(x + far * (i == j) for j, x in enumerate(good))) == 0
+
+
+def test_sizes_that_the_binding_does_not_ask_about_are_not_split():
+    size = lib().attn_prefill_packed_workspace_size
+    for B, Tq, Hq, Hkv in ((1, 1, 1, 1), (1, 300, 16, 1), (2, 18, 8, 2), (40, 40, 2, 2), (148, 148, 1, 1)):
+        for D in (64, 128):
+            assert all(size(B, Tq, Hq, Hkv, D, n) == 0 for n in (0, 1, 127, 128, 256, 383, 384))
