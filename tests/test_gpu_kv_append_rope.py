@@ -143,6 +143,52 @@ def test_rotating_append_into_an_8_bit_cache(case):
     assert np.array_equal(kp.cpu().numpy(), want_k)
 
 
+MANY = [
+    # as CASES, with so many tokens that a warp takes 4 steps of a token's rows: 1 to 4 warps a token, the last not full
+    (5, 5, 16, 16, 16, [2600], [2600], False),         # 15 rows, 32 a step: one step in all
+    (40, 20, 16, 16, 32, [1900, 700], [2000, 700], True),
+    (6, 2, 96, 96, 16, [900, 400], [950, 400], True),
+    (4, 2, 80, 0, 16, [1500], [1500], False),
+    (3, 1, 256, 256, 16, [1000], [1100], False),
+    (7, 3, 256, 128, 64, [300, 1, 400], [301, 77, 400], True),
+    (2, 2, 512, 128, 24, [200, 300], [200, 364], True),
+    (9, 2, 512, 512, 16, [250], [250], False),
+]
+
+
+@pytest.mark.parametrize("fp8_scales", [None, (0.013, 0.004)], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("case", MANY, ids=[str(c) for c in MANY])
+def test_rotating_append_of_many_tokens_at_any_head_dim(case, fp8_scales):
+    Hq, Hkv, D, rot, page, new, lens, inter = case
+    assert sum(new) * -(-(Hq + 2 * Hkv) // (512 // D)) > 148 * 16      # steps of all tokens: more than 16 an SM
+    q, k, v, p, table = make(case, seed=sum(lens) + D, fp8_scales=fp8_scales)
+    kp, vp = p.k_pool.cuda(), p.v_pool.cuda()
+    scales = dict(zip(("k_scale", "v_scale"), fp8_scales)) if fp8_scales else {}
+    k_out = torch.full(k.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    q_out = call(q, k, v, kp, vp, table, p, cumulative(new), interleaved=inter, k_out=k_out, **scales)
+    rows, turned, phys, slot = expected(case, q, k, v, p, table)
+    assert len(rows) == sum(new)
+    close(f64(q_out)[rows], *turned["q"], "q_out")
+    close(f64(k_out)[rows], *turned["k"], "k_out")
+    kept = lambda pool: bits(pool) if not fp8_scales else pool.cpu().numpy()  # noqa: E731
+    stored = lambda x, scale: bits(x) if not fp8_scales else fp8.quantize(x, scale)  # noqa: E731
+    want_v = kept(p.v_pool).copy()
+    want_v[phys, :, slot] = stored(v, fp8_scales and fp8_scales[1])[rows]
+    assert np.array_equal(kept(vp), want_v)
+    got_k = kept(kp)[phys, :, slot]
+    if fp8_scales:   # the bound of test_rotating_append_into_an_8_bit_cache
+        ks, (value, mag) = fp8_scales[0], turned["k"]
+        near, err = np.clip(value / ks, -448, 448), (2.0 ** -23 * mag + 2.0 ** -22 * np.abs(value)) / ks
+        off = np.abs(fp8.e4m3_value(kp.cpu())[phys, :, slot] - near)
+        assert (off <= np.maximum(np.abs(near) * 2.0 ** -4, 2.0 ** -10) + err * (1 + 2.0 ** -4)).all()
+    else:
+        assert np.array_equal(got_k, bits(k_out)[rows])
+    want_k = kept(p.k_pool).copy()
+    want_k[phys, :, slot] = got_k
+    want_k[phys, :, slot, rot:] = stored(k, fp8_scales and fp8_scales[0])[rows][..., rot:]
+    assert np.array_equal(kept(kp), want_k)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_in_place_on_slices_of_a_fused_projection(inter):
     Hq, Hkv, D, page, new, lens = 8, 2, 128, 16, [40, 3, 90], [100, 3, 90]

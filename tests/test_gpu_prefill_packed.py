@@ -667,3 +667,30 @@ def test_only_key_tiles_in_the_window_are_worth_a_split(Hq, Hkv, D, page, new, w
     assert api.attn_device_status(clear=True) == 0
     assert bool((ws != 0xA5).any()) == split
     assert_packed(got, packed_attention(f64(q), K, V, cu_q.tolist(), cu_k.tolist(), D ** -0.5, True, window))
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,B,Tq,live", [
+    (8, 2, 128, 64, 64, {5: (9, 5000), 63: (9, 4100)}),                      # most slots of a decode batch idle
+    (32, 8, 128, 64, 2048, {0: (16, 3000), 17: (16, 2000), 40: (16, 1), 41: (1, 700)}),
+    (12, 12, 64, 300, 900, {299: (1, 6000), 100: (300, 300), 150: (0, 800)}),
+    (4, 1, 64, 2000, 2000, {1999: (3, 2500)}),
+])
+def test_idle_slots_beside_long_live_sequences(Hq, Hkv, D, B, Tq, live):
+    """A batch and buffers for the largest step, of which a few sequences are live; the rest has no tokens, and half of
+    it no cache either."""
+    new, lens = [0] * B, [7 * (b % 2) for b in range(B)]
+    for b, (n, L) in live.items():
+        new[b], lens[b] = n, L
+    p = inputs.paged_inputs(B, Hq, Hkv, D, 16, seed=B, seq_lens=lens, spare_pages=3, poison=True)
+    q = inputs.normal((Tq, Hq, D), 3)
+    q[sum(new):] = float("nan")
+    cu = cumulative(new)
+    out, lse = torch.full((Tq, Hq, D), 3.5, dtype=torch.bfloat16, device="cuda"), torch.full((Tq, Hq), -7.25, device="cuda")
+    api.attn_device_status(clear=True)
+    api.attn_prefill_packed_paged(q.cuda(), p.k_pool.cuda(), p.v_pool.cuda(), cu.cuda(), p.page_table.cuda(),
+                                  p.seq_lens.cuda(), max_seq_len=max(lens), out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert api.attn_device_status(clear=True) == 0
+    K, V = gathered(p, lens)
+    assert_packed((out, lse), packed_attention(f64(q), K, V, cu.tolist(), cumulative(lens).tolist(), D ** -0.5))
+    assert (out[sum(new):] == 3.5).all() and (lse[sum(new):] == -7.25).all()
