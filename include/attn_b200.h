@@ -277,8 +277,10 @@ attn_status_t attn_prefill_paged(const void* q, const void* k_pool, const void* 
  *          attn_prefill_packed_workspace_size(B, Tq, Hq, Hkv, D, ceil(Tk / B))
  *          bytes, 16-byte aligned.  With it, a call with few query rows over long
  *          sequences deals each row's keys to several SMs and joins the parts
- *          (the split depends on the sizes in that call alone).  Contents are not
- *          needed between calls; two calls in flight at once need two.
+ *          (the split depends on the sizes in that call and the window alone, with
+ *          all sequences taken as equally long: a batch of many idle slots, or a Tq far
+ *          above the rows in use, is not split, and its long rows take one SM each).
+ *          Contents are not needed between calls; two calls in flight at once need two.
  * B at most 65535; Tq and Tk at most 2^30 rows.  With Tk above 2^18 (over the
  * cache: max_seq_len and the page table) and no window that keeps rows below that,
  * rows are summed in runs of 2^16 keys, so that their sums hold at any length.
@@ -632,6 +634,7 @@ attn_status_t attn_kv_append_fp8(const void* k_new, const void* v_new, uint8_t* 
  *         (T a multiple of B; one decode step is T = B)
  * page_table [B, max_pages], seq_lens [B], page_size (a multiple of 8) : as
  *         attn_kv_append
+ * B, T or Hkv 0: nothing is done (q_out is not written either).
  * B at most 2^30; D a multiple of 16, at most 512; rot_dim a multiple of 16, 0 .. D (0: a plain
  *         packed append, cos_sin may be NULL).
  * Rows that no sequence holds, and tokens at positions below 0, are skipped:

@@ -22,7 +22,8 @@
 // chain (sequence, length, then page and angles) is the latency of a
 // small call.  Blocks of 2 warps, 12 of them on an SM: 24 warps keep 96 KB of
 // loads in flight, where the registers of a free choice left 16 warps (130 us
-// on 30.6 k tokens, 768 MB, against 117 us, 6.5 TB/s, the measured copy rate), and
+// on 30.6 k tokens, 768 MB, against 117 us, 6.5 TB/s, the measured copy rate; at 80
+// registers the interleaved form spills 8 bytes), and
 // blocks of 8 warps end less evenly (24.6 us on 5.4 k tokens, 134 MB, against 23.3).
 #include <type_traits>
 

@@ -26,11 +26,13 @@
 // Stage g holds V of tile g - 1 and K of tile g, because the MMA thread uses
 // them together: P V of one tile, then S of the next, for query tile 0 and then
 // 1.  One full and one empty barrier serve two loads, and the next item's first
-// K comes with the last V of the item before.  That thread's own instructions
-// are what paces D = 128 (it never waits for a P in a long item: about 60 cycles
-// go by per MMA, 100 per wait, also for one already complete, and 40 to 60 per
-// commit, 2980 a key tile, of which the products themselves need 2048); with
-// a barrier for each load it took 5 % longer.
+// K comes with the last V of the item before.  Within a long item that thread never
+// waits for a P: a key tile of the pair takes it 2980 cycles, 2048 of them the tensor
+// pipe's own (32 MMAs of 64) and the rest its waits (about 100 each, also where
+// the phase is complete) and commits (40 to 60); with a barrier for each load it took
+// 5 % longer.  The softmax chain of a tile is nearly as long, and an item costs 4.1 us
+// beside its tiles (first softmax, last P V, output): tensor pipe 53 % active on
+// four prompts of 1733 to 4096 tokens, where 2048 of 2980 would be 69 %.
 // At D = 64 a stage is a single K or V tile: S_i(j + 1) runs ahead of P_i(j) V_j, and
 // would only wait longer for a V that it does not need (6 % on items of 2 key tiles).
 // Tail.  The last key tile of a sequence is followed in memory by the next
@@ -43,7 +45,8 @@
 //
 // Split.  With so few items that each could have several SMs (a few new tokens
 // of a few sequences), the key tiles of an item are dealt to 2 to 16 items
-// (SPLIT kernels; packed_splits has the rule and what it measured).  Each writes its
+// (SPLIT kernels; packed_splits has the rule and what it measured; at D = 64 they spill one
+// 8-byte value, read back 80 times in the code).  Each writes its
 // normalised fp32 output rows and base-2 log-sum-exps to the caller's workspace,
 // and prefill_packed_combine_kernel joins them.
 //
